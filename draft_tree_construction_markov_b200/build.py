@@ -15,13 +15,13 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdtree.so")
 SOURCES = ["api_build.cu", "markov_gemm.cu", "frontier.cu", "accept.cu", "verify_attn.cu",
            "treeflash.cu", "attn_tc.cu", "accept_noalloc.cu", "load_policy.cu", "pbuild.cu",
-           "calibration.cu"]
+           "calibration.cu", "kv_cache.cu", "paged_attn.cu", "logits.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17", "--shared", "-Xcompiler", "-fPIC",
     "-I" + os.path.join(ROOT, "include"), "-I" + CSRC,
-    "--expt-relaxed-constexpr",
+    "--expt-relaxed-constexpr", "--threads", "0",
 ]
 
 

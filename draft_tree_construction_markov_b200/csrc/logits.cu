@@ -1,0 +1,335 @@
+// Penalties for repeated tokens, biases and grammar masks on target logits.
+//
+// A CTA owns a slice of the vocabulary for one request and some of its rows.
+// It first counts the request's history into a shared-memory table of its
+// slice (one word per token: generated count, prompt flag), together with the
+// slice's bias entries and the tree nodes whose token falls in it, and marks
+// every token that any of these touch in a bitmap.  Then it streams the rows:
+// a thread takes 8 neighbouring tokens (one 16-byte load of bf16), one byte
+// of the bitmap and one byte of the row's mask.  Most groups are untouched and
+// are copied; a touched token's count is the table's plus the nodes of the list
+// that hold it and lie on the row's path (a bit of the row's ancestor word).
+// Groups the mask forbids whole are written without being read, and in place
+// an untouched, allowed group is neither read nor written.
+//
+// Bound: memory, each live row read and written once; the history is re-read
+// by every slice of its request, from L2.
+#include "common.cuh"
+
+namespace dt {
+namespace {
+
+constexpr int kLgThreads = 256;
+constexpr int kLgSlice = 4096;                 // tokens per CTA
+constexpr int kLgTab = kLgSlice + 8;           // rows start up to 7 tokens into a group of 8
+constexpr int kLgWords = (kLgTab + 31) / 32 + 1;
+constexpr int kLgGroups = kLgSlice / 8 / kLgThreads;  // groups per thread and row
+
+struct LogitsArgs {
+  const void* in;
+  void* out;
+  const int32_t* tokens;
+  const uint64_t* anc;
+  const int32_t* n_nodes;
+  int batch, Nmax, V;
+  const int32_t* hist;
+  const int32_t* hist_start;
+  const int32_t* n_prompt;
+  int n_hist;
+  const float* rep;
+  const float* pres;
+  const float* freq;
+  const int32_t* bias_start;
+  const int32_t* bias_token;
+  const float* bias_value;
+  int n_bias;
+  const uint32_t* mask;
+  const int32_t* mask_row;
+  int n_mask_rows;
+  int32_t* status;
+};
+
+// bits t .. t + 7 of a bit array of nw words; bits outside it are 0
+__device__ __forceinline__ uint32_t bits8(const uint32_t* p, int t, int nw) {
+  const int w = t >> 5, sh = t & 31;
+  const uint32_t lo = (w >= 0 && w < nw) ? p[w] : 0u;
+  const uint32_t hi = (sh > 24 && w + 1 < nw) ? p[w + 1] : 0u;
+  return __funnelshift_r(lo, hi, sh) & 0xffu;
+}
+
+// the range [s, e) of request b in a list of n entries; an impossible one is
+// recorded and empty
+__device__ __forceinline__ int2 list_range(const int32_t* start, int b, int n, int32_t* status) {
+  const int s = start[b], e = start[b + 1];
+  if (s < 0 || e < s || e > n) {
+    set_status(status, DT_EDEVICE);
+    return make_int2(0, 0);
+  }
+  return make_int2(s, e);
+}
+
+// grid (slices, batch, row groups)
+template <bool BF16, bool INPLACE>
+__global__ void __launch_bounds__(kLgThreads) logits_kernel(LogitsArgs a) {
+  constexpr int W = BF16 ? 4 : 8;  // 32-bit words of a group of 8 tokens
+  __shared__ uint32_t cnt[kLgTab];
+  __shared__ uint32_t bidx[kLgTab];
+  __shared__ uint32_t touched[kLgWords];
+  __shared__ int node_tok[64], node_id[64];
+  __shared__ int n_list;
+  const int tid = threadIdx.x, b = blockIdx.y;
+  const int base = blockIdx.x * kLgSlice - 8;  // token of table entry 0
+  int n = 0;
+  if (a.n_nodes) {
+    n = a.n_nodes[b];
+    if (n < 0 || n > a.Nmax) {
+      if (tid == 0) set_status(a.status, DT_EDEVICE);
+      n = min(max(n, 0), a.Nmax);
+    }
+  }
+  if ((int)blockIdx.z > n) return;  // uniform: none of this CTA's rows is live
+
+  // ---- the slice's table
+  for (int i = tid; i < kLgTab; i += kLgThreads) cnt[i] = bidx[i] = 0;
+  if (tid == 0) n_list = 0;
+  if (tid < kLgWords) touched[tid] = 0;
+  __syncthreads();
+  if (a.hist) {
+    const int2 r = list_range(a.hist_start, b, a.n_hist, a.status);
+    const int np = a.n_prompt ? min(max(a.n_prompt[b], 0), r.y - r.x) : 0;
+    for (int i = r.x + tid; i < r.y; i += kLgThreads) {
+      const int x = a.hist[i];
+      if (x < 0 || x >= a.V) {
+        set_status(a.status, DT_EDEVICE);
+      } else if ((uint32_t)(x - base) < (uint32_t)kLgTab) {
+        if (i - r.x < np)
+          atomicOr(&cnt[x - base], 0x80000000u);
+        else
+          atomicAdd(&cnt[x - base], 1u);
+      }
+    }
+  }
+  int2 br = make_int2(0, 0);
+  if (a.bias_start) {
+    br = list_range(a.bias_start, b, a.n_bias, a.status);
+    for (int i = br.x + tid; i < br.y; i += kLgThreads) {
+      const int x = a.bias_token[i];
+      if (x < 0 || x >= a.V)
+        set_status(a.status, DT_EDEVICE);
+      else if ((uint32_t)(x - base) < (uint32_t)kLgTab)
+        atomicMax(&bidx[x - base], (uint32_t)(i - br.x + 1));  // the last entry counts
+    }
+  }
+  if (tid < n) {
+    const int x = a.tokens[(int64_t)b * a.Nmax + tid];
+    if (x < 0 || x >= a.V) {
+      set_status(a.status, DT_EDEVICE);
+    } else if ((uint32_t)(x - base) < (uint32_t)kLgTab) {
+      const int k = atomicAdd(&n_list, 1);
+      node_tok[k] = x;
+      node_id[k] = tid;
+      atomicOr(&touched[(x - base) >> 5], 1u << ((x - base) & 31));
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < (kLgWords - 1) * 32; i += kLgThreads) {
+    const bool t = i < kLgTab && (cnt[i] | bidx[i]);
+    const uint32_t w = __ballot_sync(0xffffffffu, t);
+    if ((tid & 31) == 0 && w) atomicOr(&touched[i >> 5], w);
+  }
+  __syncthreads();
+  const int nl = n_list;
+  const float rep = a.rep ? a.rep[b] : 1.f, pres = a.pres ? a.pres[b] : 0.f,
+              freq = a.freq ? a.freq[b] : 0.f;
+  const int nw = (a.V + 31) / 32;
+
+  // ---- the rows
+  for (int i = blockIdx.z; i <= n; i += gridDim.z) {
+    const int64_t row = (int64_t)b * (a.Nmax + 1) + i;
+    const int64_t R = row * a.V;
+    const int off = (int)(R & 7);  // groups of 8 are aligned in memory
+    const uint64_t on = i ? a.anc[(int64_t)b * a.Nmax + i - 1] : 0ull;
+    const uint32_t* mask = nullptr;
+    if (a.mask) {
+      const int64_t m = a.mask_row ? a.mask_row[row] : row;
+      if (m < -1 || m >= a.n_mask_rows) {
+        if (tid == 0) set_status(a.status, DT_EDEVICE);
+      } else if (m >= 0) {
+        mask = a.mask + m * nw;
+      }
+    }
+    // one touched token's value
+    auto settle = [&](float z, int x) {
+      const uint32_t c = cnt[x - base];
+      uint32_t made = c & 0x7fffffffu;
+      for (int k = 0; k < nl; ++k)
+        if (node_tok[k] == x && ((on >> node_id[k]) & 1ull)) ++made;
+      if (made || (c >> 31)) z = z > 0.f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
+      if (made) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, (float)made)), pres);
+      const uint32_t bi = bidx[x - base];
+      if (bi) z = __fadd_rn(z, a.bias_value[br.x + bi - 1]);
+      return z;
+    };
+    uint32_t u[kLgGroups][W];
+    uint32_t tb[kLgGroups], mb[kLgGroups];
+#pragma unroll
+    for (int j = 0; j < kLgGroups; ++j) {
+      const int t0 = (blockIdx.x * (kLgSlice / 8) + j * kLgThreads + tid) * 8 - off;
+      const bool full = t0 >= 0 && t0 + 8 <= a.V;
+      tb[j] = bits8(touched, t0 - base, kLgWords);
+      mb[j] = 0xffu;
+      if (mask) mb[j] = bits8(mask, t0, nw);
+      const bool need = full && mb[j] != 0 && !(INPLACE && tb[j] == 0 && mb[j] == 0xffu);
+      if (need) {
+        const uint4* p = (const uint4*)((const uint8_t*)a.in + (R + t0) * (BF16 ? 2 : 4));
+#pragma unroll
+        for (int w = 0; w < W / 4; ++w) {
+          const uint4 q = p[w];
+          u[j][4 * w] = q.x, u[j][4 * w + 1] = q.y, u[j][4 * w + 2] = q.z, u[j][4 * w + 3] = q.w;
+        }
+      } else {
+#pragma unroll
+        for (int w = 0; w < W; ++w) u[j][w] = 0;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kLgGroups; ++j) {
+      const int t0 = (blockIdx.x * (kLgSlice / 8) + j * kLgThreads + tid) * 8 - off;
+      if (t0 >= 0 && t0 + 8 <= a.V) {
+        if (INPLACE && tb[j] == 0 && mb[j] == 0xffu) continue;
+        uint32_t t = tb[j] & mb[j];
+        while (t) {
+          const int e = __ffs(t) - 1;
+          t &= t - 1;
+          const int wi = BF16 ? e >> 1 : e;
+          uint32_t word = 0;
+#pragma unroll
+          for (int w = 0; w < W; ++w)
+            if (w == wi) word = u[j][w];
+          if (BF16) {
+            const int sh = 16 * (e & 1);
+            const float z = settle(__uint_as_float((word >> sh) << 16), t0 + e);
+            uint32_t r;
+            asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(r) : "f"(z));
+            word = (word & (0xffff0000u >> sh)) | ((r & 0xffffu) << sh);
+          } else {
+            word = __float_as_uint(settle(__uint_as_float(word), t0 + e));
+          }
+#pragma unroll
+          for (int w = 0; w < W; ++w)
+            if (w == wi) u[j][w] = word;
+        }
+        if (mb[j] != 0xffu) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (BF16) {
+              if (!((mb[j] >> e) & 1u))
+                u[j][e >> 1] = (e & 1) ? (u[j][e >> 1] & 0x0000ffffu) | 0xff800000u
+                                       : (u[j][e >> 1] & 0xffff0000u) | 0x0000ff80u;
+            } else if (!((mb[j] >> e) & 1u)) {
+              u[j][e] = 0xff800000u;
+            }
+          }
+        }
+        uint4* p = (uint4*)((uint8_t*)a.out + (R + t0) * (BF16 ? 2 : 4));
+#pragma unroll
+        for (int w = 0; w < W / 4; ++w)
+          p[w] = make_uint4(u[j][4 * w], u[j][4 * w + 1], u[j][4 * w + 2], u[j][4 * w + 3]);
+      } else if (t0 + 8 > 0 && t0 < a.V) {
+        // a group cut by the row's start or end: token by token
+        for (int e = 0; e < 8; ++e) {
+          const int x = t0 + e;
+          if (x < 0 || x >= a.V) continue;
+          const int64_t at = R + x;
+          float z = BF16 ? bf16_to_f32(((const uint16_t*)a.in)[at]) : ((const float*)a.in)[at];
+          if ((tb[j] >> e) & 1u) z = settle(z, x);
+          if (!((mb[j] >> e) & 1u)) z = -INFINITY;
+          if (BF16) {
+            uint32_t r;
+            asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(r) : "f"(z));
+            ((uint16_t*)a.out)[at] = (uint16_t)r;
+          } else {
+            ((float*)a.out)[at] = z;
+          }
+        }
+      }
+    }
+  }
+}
+
+}  // namespace
+}  // namespace dt
+
+using namespace dt;
+
+extern "C" {
+
+size_t dt_logits_workspace_bytes(void) { return kWsHeader; }
+
+dt_status dt_logits_process(const void* d_logits, dt_dtype dt, const int32_t* d_tokens,
+                            const uint64_t* d_anc, const int32_t* d_n_nodes, int batch, int Nmax,
+                            int V, const int32_t* d_history, const int32_t* d_hist_start,
+                            const int32_t* d_n_prompt, int n_history, const float* d_repetition,
+                            const float* d_presence, const float* d_frequency,
+                            const int32_t* d_bias_start, const int32_t* d_bias_token,
+                            const float* d_bias_value, int n_bias, const uint32_t* d_mask,
+                            const int32_t* d_mask_row, int n_mask_rows, void* d_out, void* ws,
+                            size_t ws_bytes, dt_stream stream) {
+  if (!d_logits || !d_out || (dt != DT_F32 && dt != DT_BF16)) return DT_EINVAL;
+  if (batch < 1 || Nmax < 0 || V < 1 || n_history < 0 || n_bias < 0 || n_mask_rows < 0)
+    return DT_EINVAL;
+  const bool tree = d_tokens && d_anc && d_n_nodes;
+  if (Nmax > 0 ? !tree : (d_tokens || d_anc || d_n_nodes)) return DT_EINVAL;
+  if (!d_history != !d_hist_start || (d_n_prompt && !d_history)) return DT_EINVAL;
+  if (!d_bias_start != !d_bias_token || !d_bias_start != !d_bias_value) return DT_EINVAL;
+  if (d_mask_row && !d_mask) return DT_EINVAL;
+  if (((uintptr_t)d_logits | (uintptr_t)d_out) & 15) return DT_EINVAL;
+  if (Nmax > 64 || batch > 1024 || V >= 1 << 24) return DT_EUNSUPPORTED;
+  const size_t bytes = (size_t)batch * (Nmax + 1) * V * (dt == DT_BF16 ? 2 : 4);
+  const uintptr_t x = (uintptr_t)d_logits, y = (uintptr_t)d_out;
+  if (x != y && x < y + bytes && y < x + bytes) return DT_EINVAL;  // partial overlap
+  if (!ws || ws_bytes < kWsHeader) return DT_EWORKSPACE;
+  LogitsArgs a;
+  a.in = d_logits;
+  a.out = d_out;
+  a.tokens = d_tokens;
+  a.anc = d_anc;
+  a.n_nodes = d_n_nodes;
+  a.batch = batch;
+  a.Nmax = Nmax;
+  a.V = V;
+  a.hist = d_history;
+  a.hist_start = d_hist_start;
+  a.n_prompt = d_n_prompt;
+  a.n_hist = n_history;
+  a.rep = d_repetition;
+  a.pres = d_presence;
+  a.freq = d_frequency;
+  a.bias_start = d_bias_start;
+  a.bias_token = d_bias_token;
+  a.bias_value = d_bias_value;
+  a.n_bias = n_bias;
+  a.mask = d_mask;
+  a.mask_row = d_mask_row;
+  a.n_mask_rows = n_mask_rows;
+  a.status = (int32_t*)ws;
+  // a row may start 7 tokens into its first group of 8
+  const int slices = (V + 7 + kLgSlice - 1) / kLgSlice;
+  const int rows = Nmax + 1;
+  // rows are split over CTAs until there are about six per SM
+  const int want = (6 * dt_num_sms() + slices * batch - 1) / (slices * batch);
+  const int z = want < 1 ? 1 : want > rows ? rows : want;
+  const dim3 grid(slices, batch, z);
+  cudaStream_t s = (cudaStream_t)stream;
+  ProfileScope ps(DT_K_LOGITS, s);
+  const bool in_place = d_logits == d_out;
+  if (dt == DT_BF16)
+    in_place ? logits_kernel<true, true><<<grid, kLgThreads, 0, s>>>(a)
+             : logits_kernel<true, false><<<grid, kLgThreads, 0, s>>>(a);
+  else
+    in_place ? logits_kernel<false, true><<<grid, kLgThreads, 0, s>>>(a)
+             : logits_kernel<false, false><<<grid, kLgThreads, 0, s>>>(a);
+  return cudaGetLastError() == cudaSuccess ? DT_OK : DT_ECUDA;
+}
+
+}  // extern "C"

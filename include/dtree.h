@@ -13,6 +13,12 @@
  *                       over several GPUs (partials all-gathered per wave)
  *   dt_tree_verify_attn tree-masked grouped-query attention over prefix + tree
  *   dt_tree_accept      lossless acceptance walk (greedy or recursive residual)
+ *   dt_kv_write/_commit/_read  a paged, optionally quantised KV cache: rows
+ *                       quantised as they enter it, and read back
+ *   dt_paged_attn       attention of a chunk of new tokens over that cache
+ *   dt_tree_verify_attn_paged  the tree-masked attention over that cache
+ *   dt_logits_process   penalties, biases and grammar masks on target logits,
+ *                       per node of a tree
  *
  * Conventions shared by every entry point
  *   - Pointers named d_* are DEVICE pointers; the caller owns every buffer.
@@ -57,7 +63,9 @@ typedef enum {
   DT_EDEVICE = 6        /* a device-side range check failed                   */
 } dt_status;
 
-typedef enum { DT_F32 = 0, DT_BF16 = 1 } dt_dtype;
+/* DT_E4M3 (8-bit float, 4 exponent and 3 mantissa bits, largest value 448) and
+ * DT_I8 are types of a KV cache only. */
+typedef enum { DT_F32 = 0, DT_BF16 = 1, DT_E4M3 = 2, DT_I8 = 3 } dt_dtype;
 
 typedef void* dt_stream; /* cudaStream_t */
 
@@ -425,6 +433,169 @@ dt_status dt_calib_fit(const int32_t* d_depth, const float* d_ell, const int8_t*
                        float* d_calib, double* d_loglik, void* ws, size_t ws_bytes,
                        dt_stream stream);
 
+/* ------------------------------------------------------- paged KV cache --
+ * What a serving program keeps beside the round: every request's keys and
+ * values in fixed-size pages of one pool.  Position p of request b is slot
+ * p % page_size of page d_page_table[b][p / page_size]; a page holds each KV
+ * head's rows together.  A DT_E4M3 or DT_I8 cache stores one code per value
+ * and one fp32 scale per (position, KV head), a value being code * scale.
+ *
+ * Shared by the calls below (the articles that the round follows say nothing
+ * about a cache or sampling settings; a round only needs them to be there):
+ *   limits   head_dim in {64, 128}; page_size 8, 16, 32, 64, 128 or 256;
+ *            batch <= 1024; Hq a multiple of Hkv; Hkv <= 1024; n_pages *
+ *            Hkv * page_size < 2^31, max_pages * page_size < 2^30,
+ *            total_rows * Hq < 2^30
+ *   base pointers of K, V and the cache arrays 16-byte aligned
+ *   ws       its first 256 bytes cleared before the first use.  These calls
+ *            leave the status word as it is unless they record an error, so
+ *            dt_read_status() reports (and clears) the first of any number
+ *            of calls.
+ *   a position outside the page table's row, or a page index outside
+ *            [0, n_pages), of a position that the call needs records
+ *            DT_EDEVICE; a write there is dropped, a read gives zeros.
+ *            Entries of pages that no row of the call sees are not read. */
+typedef struct {
+  void* d_k;         /* [n_pages][Hkv][page_size][d], type dt               */
+  void* d_v;
+  float* d_k_scale;  /* [n_pages][Hkv][page_size]; DT_E4M3 and DT_I8 only   */
+  float* d_v_scale;
+  int n_pages, page_size, Hkv, d;
+  dt_dtype dt;       /* DT_F32, DT_BF16, DT_E4M3 or DT_I8                   */
+} dt_kv_cache;
+
+size_t dt_kv_workspace_bytes(void);
+
+/* Quantises the rows of new tokens as they enter the cache.  Row i of request
+ * b (row d_row_start[b] + i of d_k/d_v, up to d_row_start[b + 1]) goes to
+ * position d_pos[b] + i.  With a = max(max_d |x|, 2^-100) and X = 448
+ * (DT_E4M3) or 127 (DT_I8), all in fp32 to nearest even:
+ *   scale = a / X,   code = round(x * (X / a))   (clamped to [-X, X])
+ * A row of a head that holds an infinity or a NaN gets scale NaN and codes 0,
+ * so that all of it reads as NaN.  DT_BF16 and DT_F32 caches take the value,
+ * rounded once.
+ *   d_k, d_v     [total_rows][Hkv][d] fp32 or bf16 (dt); rows are ld_k and
+ *                ld_v elements apart (a slice of a fused projection will do)
+ *   d_row_start  [batch + 1], non-decreasing within [0, total_rows]
+ *   d_pos        [batch] first position of each request, >= 0
+ * Positions that one call writes must be distinct. */
+dt_status dt_kv_write(const void* d_k, const void* d_v, int64_t ld_k, int64_t ld_v, dt_dtype dt,
+                      const int32_t* d_row_start, const int32_t* d_pos,
+                      const int32_t* d_page_table, int max_pages, int batch, int total_rows,
+                      const dt_kv_cache* cache, void* ws, size_t ws_bytes, dt_stream stream);
+
+/* The same for what a round accepted: the root's tree row and the rows of the
+ * nodes d_acc_nodes[b][0 .. d_n_acc[b]) of dt_tree_accept go to the
+ * positions d_pos[b], d_pos[b] + 1, ...
+ *   d_k_tree, d_v_tree  [batch][Nmax+1][Hkv][d] (row 0 = root, i+1 = node i) */
+dt_status dt_kv_commit(const void* d_k_tree, const void* d_v_tree, dt_dtype dt,
+                       const int32_t* d_acc_nodes, const int32_t* d_n_acc, int Bk, int Nmax,
+                       const int32_t* d_pos, const int32_t* d_page_table, int max_pages,
+                       int batch, const dt_kv_cache* cache, void* ws, size_t ws_bytes,
+                       dt_stream stream);
+
+/* Reads positions d_pos[b] + i back into the packed rows d_row_start[b] + i of
+ * d_k_out/d_v_out [total_rows][Hkv][d] fp32 or bf16 (dt), the layout that
+ * dt_tree_verify_attn takes as its prefix; code * scale is rounded once.
+ * Rows outside every request's range are left as they were. */
+dt_status dt_kv_read(const dt_kv_cache* cache, const int32_t* d_page_table, int max_pages,
+                     const int32_t* d_row_start, const int32_t* d_pos, int batch, int total_rows,
+                     dt_dtype dt, void* d_k_out, void* d_v_out, void* ws, size_t ws_bytes,
+                     dt_stream stream);
+
+/* Causal grouped-query attention of a chunk of new tokens over the cache, for
+ * prompts in pieces and for single tokens alike.  The chunk's own keys and
+ * values are in the cache already (dt_kv_write): request b has d_kv_len[b]
+ * positions, the last of which are its n = d_row_start[b+1] - d_row_start[b]
+ * rows, so row i sits at position p = d_kv_len[b] - n + i and sees the
+ * positions j <= p, with window > 0 only those with j > p - window or
+ * j < n_sink (the first tokens stay visible).
+ *   out[row][h] = sum_j softmax_j(scale * q[row][h] . k_j) v_j,
+ * head h using KV head h / (Hq / Hkv); a row that sees nothing (p < 0) is 0.
+ *   d_q    [total_rows][Hq][d], rows ld_q elements apart; d_out the same,
+ *          contiguous; both bf16 (dt = DT_BF16; any cache but DT_F32) or fp32
+ *   max_rows  no request has more rows; it decides how the work is split
+ *   window >= 0 (0: no window), n_sink >= 0 (ignored without a window)
+ * Rows outside every request's range are left as they were.  Scores, softmax
+ * statistics and sums are fp32; the softmax weights enter the second product
+ * as bf16 (dt = DT_BF16).  A request longer than its page table's row, with
+ * more than max_rows rows, or with a negative length records DT_EDEVICE and
+ * its rows are left as they were. */
+size_t dt_paged_attn_workspace_bytes(int batch, int total_rows, int Hq, int Hkv, int d);
+
+dt_status dt_paged_attn(const void* d_q, int64_t ld_q, const int32_t* d_row_start,
+                        const dt_kv_cache* cache, const int32_t* d_page_table, int max_pages,
+                        const int32_t* d_kv_len, int batch, int total_rows, int max_rows, int Hq,
+                        float scale, int window, int n_sink, dt_dtype dt, void* d_out, void* ws,
+                        size_t ws_bytes, dt_stream stream);
+
+/* dt_tree_verify_attn over the paged cache: row i of request b sees the
+ * cached positions [0, d_prefix_len[b]), the root's tree row and the tree rows
+ * of its ancestors and itself.  The tree's keys and values stay outside the
+ * cache (type dt, not quantised) until dt_kv_commit.  With window > 0 a row at
+ * depth e (0 for the root, d_depths[b][i-1] for row i) sees the cached
+ * positions j > d_prefix_len[b] + e - window and j < n_sink; the window
+ * must be larger than Nmax, so that it never cuts the tree itself, and d_depths
+ * may be NULL without one.
+ *   d_q, d_out [batch][Nmax+1][Hq][d]; d_k_tree, d_v_tree [batch][Nmax+1][Hkv][d]
+ *   d_anc, d_depths [batch][Nmax], d_n_nodes [batch] of the dt_tree
+ * Rows > d_n_nodes[b] are left as they were.  Types, sums and errors as in
+ * dt_paged_attn; a node count outside [0, Nmax] records DT_EDEVICE and is
+ * clamped. */
+size_t dt_tree_verify_attn_paged_workspace_bytes(int batch, int Nmax, int Hq, int Hkv, int d);
+
+dt_status dt_tree_verify_attn_paged(const void* d_q, const dt_kv_cache* cache,
+                                    const int32_t* d_page_table, int max_pages,
+                                    const int32_t* d_prefix_len, const void* d_k_tree,
+                                    const void* d_v_tree, const uint64_t* d_anc,
+                                    const int32_t* d_depths, const int32_t* d_n_nodes, int batch,
+                                    int Nmax, int Hq, float scale, int window, int n_sink,
+                                    dt_dtype dt, void* d_out, void* ws, size_t ws_bytes,
+                                    dt_stream stream);
+
+/* ----------------------------------------------------- logits processing --
+ * What a request's sampling settings do to the target's logits, before
+ * dt_tree_accept reads them: every row of a tree is the distribution after its
+ * own path, so the counts of a row are those of the request's history plus the
+ * tokens from the root's child down to the row's node.  For token x of row i
+ * (0 = root, i = node i - 1) of request b, in this order, in fp32, rounded
+ * once at the end:
+ *   c  = occurrences of x in the generated part of the history and on the path
+ *   z  = z > 0 ? z / repetition[b] : z * repetition[b]   if c > 0 or x is in
+ *        the prompt part of the history
+ *   z -= frequency[b] * c;   z -= presence[b] if c > 0
+ *   z += bias of x, if the request lists one
+ *   z  = -infinity if bit x % 32 of word x / 32 of the row's mask is 0
+ *   d_logits, d_out  [batch][Nmax+1][V] fp32 or bf16 (dt), 16-byte aligned;
+ *            d_out may be d_logits (in place) and must not overlap it otherwise
+ *   d_tokens, d_anc, d_n_nodes  of the dt_tree; with Nmax = 0 (one row per
+ *            request, no tree) all three are NULL
+ *   d_history, d_hist_start [batch+1]: request b's tokens (the root's token
+ *            among them) are d_history[d_hist_start[b] .. d_hist_start[b+1]);
+ *            its first d_n_prompt[b] are the prompt (NULL = none); both NULL:
+ *            no history.  n_history is the length of d_history.
+ *   d_repetition (> 0), d_presence, d_frequency  [batch], NULL = 1, 0, 0
+ *   d_bias_token, d_bias_value, d_bias_start [batch+1]: all NULL, or the
+ *            requests' lists (n_bias entries in all); of a token listed twice
+ *            the last entry counts
+ *   d_mask   [n_mask_rows][(V+31)/32], or NULL; row i of request b uses mask
+ *            row d_mask_row[b][i] (-1: everything allowed), or row
+ *            b * (Nmax+1) + i with d_mask_row NULL
+ * Rows > d_n_nodes[b] of d_out are left as they were.  Tokens outside [0, V),
+ * ranges outside their arrays, and mask rows outside [-1, n_mask_rows) record
+ * DT_EDEVICE and are ignored.  Limits: Nmax <= 64, batch <= 1024, V < 2^24. */
+size_t dt_logits_workspace_bytes(void);
+
+dt_status dt_logits_process(const void* d_logits, dt_dtype dt, const int32_t* d_tokens,
+                            const uint64_t* d_anc, const int32_t* d_n_nodes, int batch, int Nmax,
+                            int V, const int32_t* d_history, const int32_t* d_hist_start,
+                            const int32_t* d_n_prompt, int n_history, const float* d_repetition,
+                            const float* d_presence, const float* d_frequency,
+                            const int32_t* d_bias_start, const int32_t* d_bias_token,
+                            const float* d_bias_value, int n_bias, const uint32_t* d_mask,
+                            const int32_t* d_mask_row, int n_mask_rows, void* d_out, void* ws,
+                            size_t ws_bytes, dt_stream stream);
+
 /* Synchronises `stream` and returns the status word that device code of the
  * last call using `ws` wrote (DT_OK, DT_ETIMEOUT or DT_EDEVICE), then clears
  * it.  `ws` is the workspace passed to that call. */
@@ -446,7 +617,9 @@ typedef enum {
   DT_K_OTHER = 8,
   DT_K_TF_LMHEAD = 9,     /* TreeFlash LM head + top-M epilogue               */
   DT_K_TF_MLP = 10,       /* TreeFlash SwiGLU / down projection               */
-  DT_K_PBUILD = 11        /* every wave of a small build in one launch        */
+  DT_K_PBUILD = 11,       /* every wave of a small build in one launch        */
+  DT_K_KV = 12,           /* rows written to or read from a KV cache          */
+  DT_K_LOGITS = 13        /* logits processing                                */
 } dt_kernel_kind;
 
 /* How dt_tree_build and dt_tree_build_ex run the waves of the best-first

@@ -23,6 +23,8 @@ load_policy  survival-ordered allocation of a round's verification capacity
              over a batch (TreeSpark article, load-adaptive serving policy).
 calibration  logged (depth, log-probability, accepted) triples and the
              per-depth maximum-likelihood fit of the calibration.
+paged_attn   attention of a chunk or a tree over a paged, quantised KV cache.
+logits       penalties, biases and masks on target logits.
 
 Every floating quantity is fp64; inputs are the exact stored values.
 """
