@@ -15,7 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdtree.so")
 SOURCES = ["api_build.cu", "markov_gemm.cu", "frontier.cu", "accept.cu", "verify_attn.cu",
            "treeflash.cu", "attn_tc.cu", "accept_noalloc.cu", "load_policy.cu", "pbuild.cu",
-           "calibration.cu", "kv_cache.cu", "paged_attn.cu", "logits.cu"]
+           "calibration.cu", "kv_cache.cu", "paged_attn.cu", "paged_tc.cu", "paged_decode.cu",
+           "logits.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

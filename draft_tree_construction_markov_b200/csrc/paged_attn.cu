@@ -1,9 +1,10 @@
 // Attention over a paged KV cache: a chunk of new tokens (causal, optionally a
 // sliding window with a few first tokens kept), or a draft tree's rows.
 //
-// This file holds the C entry points and the plain kernel, one warp per (row,
-// head): 32 keys at a time a lane takes one key's score, the warp keeps the
-// running maximum and sum, and then lanes own head-dim columns of the output.
+// This file holds the C entry points and the kernel of fp32 queries, one warp
+// per (row, head); bf16 queries take the tiled kernels.
+#include <algorithm>
+
 #include "paged_attn.cuh"
 
 namespace dt {
@@ -12,20 +13,10 @@ namespace {
 constexpr int kPlainWarps = 4;
 constexpr int kMaxWindow = 1 << 30;  // no request is longer; keeps position - window in 32 bits
 
-template <int CT>
-__device__ __forceinline__ float dot_row(const void* base, int64_t at, int d, const float* q) {
-  const typename Code<CT>::T* p = (const typename Code<CT>::T*)base + at;
-  float s = 0.f;
-  for (int e = 0; e < d; ++e) s = fmaf(Code<CT>::get(p[e]), q[e], s);
-  return s;
-}
-
 // grid (total rows, ceil(Hq / 4))
 template <int CT, int DT>
 __global__ void __launch_bounds__(32 * kPlainWarps) paged_plain_kernel(PagedArgs a) {
-  __shared__ float sq[kPlainWarps][128];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = blockIdx.x, h = blockIdx.y * kPlainWarps + warp;
+  const int r = blockIdx.x, h = blockIdx.y * kPlainWarps + (threadIdx.x >> 5);
   int b, i;
   if (a.row_start) {
     b = row_request(a.row_start, a.batch, r);
@@ -35,80 +26,97 @@ __global__ void __launch_bounds__(32 * kPlainWarps) paged_plain_kernel(PagedArgs
     b = r / (a.Nmax + 1);
     i = r % (a.Nmax + 1);
   }
-  const PagedRequest rq = paged_request(a, b);
-  if (i >= rq.n || h >= a.Hq) return;
-  const int kvh = h / a.G;
-  const typename Code<DT>::T* q = (const typename Code<DT>::T*)a.q + r * a.ld_q + (int64_t)h * a.d;
-  for (int e = lane; e < a.d; e += 32) sq[warp][e] = Code<DT>::get(q[e]);
-  __syncwarp();
+  if (i < paged_request(a, b).n && h < a.Hq) paged_row<CT, DT>(a, b, i, h);
+}
 
-  const int per = a.d / 32;  // output columns of a lane: lane * per ...
-  float o[4] = {0.f, 0.f, 0.f, 0.f};
-  float m = -INFINITY, l = 0.f;
-  // 32 keys: this lane's score s (ok: it is visible), then every lane's value row
-  auto step = [&](bool ok, float s, auto value) {
-    const float top = fmaxf(m, warp_max(ok ? s : -INFINITY));
-    const float keep = m == top ? 1.f : expf(m - top);
-    // all scores so far -infinity: weights of 0
-    const float p = !ok || s == -INFINITY ? 0.f : expf(s - top);
-    l = l * keep + warp_sum(p);
-    m = top;
-    for (int x = 0; x < per; ++x) o[x] *= keep;
-    for (unsigned seen = __ballot_sync(0xffffffffu, ok); seen; seen &= seen - 1) {
-      const int k = __ffs(seen) - 1;
-      value(k, __shfl_sync(0xffffffffu, p, k));
+// Joins the shares of a row tile.  grid (workers of the tiled kernel, row parts);
+// a warp takes a row, its lanes four columns each.
+constexpr int kJoinWarps = 8, kJoinRows = 32;
+
+template <int CT>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    paged_join_kernel(const __grid_constant__ PagedArgs a, Cut cut) {
+  pdl_wait();
+  const PagedSplit sp = a.split[blockIdx.x];
+  if (sp.parts == 0) return;
+  const PagedRequest rq = paged_request(a, sp.b);
+  const RowTile t = row_tile(a, rq, sp.mt, cut);
+  const int lane = threadIdx.x & 31;
+  for (int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+       r < min(t.live, (int)(blockIdx.y + 1) * kJoinRows); r += kJoinWarps) {
+    const int i = (t.m0 + r) / a.G, h = sp.kvh * a.G + (t.m0 + r) % a.G;
+    // part 0: the second slot of the worker before; part k: the first slot of worker + k - 1
+    auto at = [&](int k) {
+      const int64_t slot = k ? 2 * ((int64_t)blockIdx.x + k - 1) : 2 * (int64_t)blockIdx.x - 1;
+      return slot * a.part_rows + r;
+    };
+    float m = -INFINITY, l = 0.f;
+    for (int k = lane; k < sp.parts; k += 32) m = fmaxf(m, a.part_ml[at(k)].x);
+    m = warp_max(m);
+    for (int k = lane; k < sp.parts; k += 32) {
+      const float2 ml = a.part_ml[at(k)];
+      l += ml.x == -INFINITY ? ml.y : ex2(ml.x - m) * ml.y;  // (a NaN sum stays one)
     }
-  };
-  const Visible vis = visible(a, row_position(a, rq, b, i), rq.len);
-  for (int part = 0; part < 2; ++part) {
-    const int lo = part ? vis.first : 0, hi = part ? vis.last : vis.sink;
-    for (int j0 = lo; j0 < hi; j0 += 32) {
-      const int j = j0 + lane;
-      const bool ok = j < hi;
-      int64_t slot = -1;
-      float s = 0.f;
-      if (ok) {
-        slot = a.c.slot(b, j, a.status);
-        if (slot >= 0) {
-          slot += (int64_t)kvh << a.c.page_shift;
-          s = dot_row<CT>(a.c.k, slot * a.d, a.d, sq[warp]) * (a.c.ks ? a.c.ks[slot] : 1.f);
-        }
-        s *= a.scale;
+    l = warp_sum(l);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (lane * 4 < a.d) {
+#pragma unroll 4
+      for (int k = 0; k < sp.parts; ++k) {
+        const float mk = a.part_ml[at(k)].x;
+        const float w = mk == -INFINITY ? 0.f : ex2(mk - m);
+        const float4 x = *(const float4*)(a.part_o + at(k) * a.d + lane * 4);
+        o.x = fmaf(w, x.x, o.x);
+        o.y = fmaf(w, x.y, o.y);
+        o.z = fmaf(w, x.z, o.z);
+        o.w = fmaf(w, x.w, o.w);
       }
-      step(ok, s, [&](int k, float p) {
-        const int64_t at = __shfl_sync(0xffffffffu, slot, k);
-        if (at < 0) return;
-        const typename Code<CT>::T* v = (const typename Code<CT>::T*)a.c.v + at * a.d + lane * per;
-        if (a.c.vs) p *= a.c.vs[at];
-        for (int x = 0; x < per; ++x) o[x] = fmaf(p, Code<CT>::get(v[x]), o[x]);
-      });
     }
+    const Visible vis = visible(a, row_position(a, rq, sp.b, i), rq.len);
+    const bool sees = a.kt || vis.sink > 0 || vis.last > vis.first;
+    const float inv = row_factor(l, sees);
+    if (lane * 4 < a.d)
+      *(uint2*)((uint16_t*)a.out + (((int64_t)rq.r0 + i) * a.Hq + h) * a.d + lane * 4) =
+          sees ? make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv))
+               : make_uint2(0u, 0u);
+    const float odd = (o.x + o.y + o.z + o.w) * 0.f;
+    if (__any_sync(0xffffffffu, sees && odd != 0.f && l - l == 0.f))
+      paged_row<CT, DT_BF16>(a, sp.b, i, h);
   }
-  if (a.kt) {
-    const uint64_t anc = i ? a.anc[(int64_t)b * a.Nmax + i - 1] : 0ull;
-    for (int j0 = 0; j0 < rq.n; j0 += 32) {
-      const int j = j0 + lane;
-      const bool ok = j < rq.n && tree_sees(anc, i, j);
-      const int64_t row0 = ((int64_t)rq.r0 * a.c.Hkv + kvh) * a.d;
-      const int64_t ld = (int64_t)a.c.Hkv * a.d;
-      const float s = ok ? dot_row<DT>(a.kt, row0 + j * ld, a.d, sq[warp]) * a.scale : 0.f;
-      step(ok, s, [&](int k, float p) {
-        const typename Code<DT>::T* v =
-            (const typename Code<DT>::T*)a.vt + row0 + (j0 + k) * ld + lane * per;
-        for (int x = 0; x < per; ++x) o[x] = fmaf(p, Code<DT>::get(v[x]), o[x]);
-      });
-    }
-  }
-  const bool any = a.kt || vis.sink > 0 || vis.last > vis.first;
-  const float inv = any ? 1.f / l : 0.f;
-  const int64_t at = ((int64_t)r * a.Hq + h) * a.d + lane * per;
-  for (int x = 0; x < per; ++x) {
-    const float y = any ? o[x] * inv : 0.f;
-    if constexpr (DT == DT_F32)
-      ((float*)a.out)[at + x] = y;
-    else
-      ((__nv_bfloat16*)a.out)[at + x] = __float2bfloat16_rn(y);
-  }
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                             const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                             const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return (EncodeFn) nullptr;
+    return (EncodeFn)p;
+  }();
+  return fn;
+}
+
+// Records, fp32 sums and statistics of the row tiles that shares cut, two per
+// worker; `all`: (row, head) pairs of a KV head that a row tile can have at most.
+struct PartPlan {
+  size_t sums, stats, bytes;  // offsets behind the header, and all
+};
+PartPlan part_plan(int64_t workers, int64_t rows, int d) {
+  PartPlan p;
+  p.sums = workers * sizeof(PagedSplit);
+  p.stats = p.sums + 2 * workers * rows * d * 4;
+  p.bytes = kWsHeader + p.stats + 2 * workers * rows * sizeof(float2);
+  return p;
+}
+size_t paged_workspace(int64_t all, int d) {
+  return std::max(part_plan(2 * kPagedSms, std::min<int64_t>(all, 128), d).bytes,
+                  part_plan(kDecodeWorkers, std::min<int64_t>(all, kDecodePairs), d).bytes);
 }
 
 template <int DT>
@@ -121,19 +129,28 @@ void launch_plain(const PagedArgs& a, int ct, dim3 grid, cudaStream_t s) {
   }
 }
 
-dt_status run_paged(const PagedArgs& a, int ct, int dt, cudaStream_t s) {
+dt_status run_paged(PagedArgs a, const dt_kv_cache* cache, int dt, void* ws, cudaStream_t s) {
   if (a.total_rows == 0) return DT_OK;
-  ProfileScope ps(DT_K_ATTN, s);
-  const dim3 grid(a.total_rows, (a.Hq + kPlainWarps - 1) / kPlainWarps);
-  if (dt == DT_F32)
+  const int ct = cache->dt;
+  if (dt == DT_F32) {
+    ProfileScope ps(DT_K_ATTN, s);
+    const dim3 grid(a.total_rows, (a.Hq + kPlainWarps - 1) / kPlainWarps);
     launch_plain<DT_F32>(a, ct, grid, s);
-  else
-    launch_plain<DT_BF16>(a, ct, grid, s);
-  return cudaGetLastError() == cudaSuccess ? DT_OK : DT_ECUDA;
-}
-
-size_t paged_workspace(int64_t total_rows, int Hq, int Hkv, int d) {
-  return kWsHeader;
+    return cudaGetLastError() == cudaSuccess ? DT_OK : DT_ECUDA;
+  }
+  const int64_t pairs = (int64_t)a.max_rows * a.G;  // of a request, for one KV head
+  const int64_t all = (int64_t)(a.kt ? a.Nmax + 1 : a.total_rows) * a.G;
+  const bool few = !a.kt && pairs <= kDecodePairs;
+  const int tiles = pairs > (a.kt ? 256 : 128) ? 2 : 1;
+  a.part_rows = (int)std::min<int64_t>(all, few ? kDecodePairs : 128 * tiles);
+  const PartPlan p = part_plan(few ? kDecodeWorkers : 2 * kPagedSms / tiles, a.part_rows, a.d);
+  uint8_t* w = (uint8_t*)ws + kWsHeader;
+  a.split = (PagedSplit*)w;
+  a.part_o = (float*)(w + p.sums);
+  a.part_ml = (float2*)(w + p.stats);
+  const cudaError_t e = few ? launch_paged_decode(a, ct, cache, (int)pairs, s)
+                            : launch_paged_tc(a, ct, cache, tiles, s);
+  return e == cudaSuccess ? DT_OK : DT_ECUDA;
 }
 
 // checks that both entry points share, after the cache's own
@@ -150,13 +167,40 @@ dt_status check_paged(const dt_kv_cache* c, const void* q, const void* out, int 
 }  // namespace
 }  // namespace dt
 
+namespace dt {
+
+bool paged_map(CUtensorMap* m, const void* base, int bytes, uint64_t cols, uint64_t rows,
+               uint32_t box) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {cols * bytes};
+  const uint32_t width = (uint32_t)std::min<uint64_t>(cols * bytes, 128);
+  const cuuint32_t boxes[2] = {width / bytes, box}, one[2] = {1, 1};
+  return fn(m, bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+            const_cast<void*>(base), dims, strides, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_paged_join(const PagedArgs& a, int ct, Cut cut, int workers, cudaStream_t s) {
+  ProfileScope ps(DT_K_ATTN_COMBINE, s);
+  const dim3 grid(workers, (a.part_rows + kJoinRows - 1) / kJoinRows);
+  auto kern = ct == DT_BF16   ? paged_join_kernel<DT_BF16>
+              : ct == DT_E4M3 ? paged_join_kernel<DT_E4M3>
+                              : paged_join_kernel<DT_I8>;
+  const cudaError_t e = launch_pdl(kern, grid, dim3(32 * kJoinWarps), 0, s, a, cut);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+}  // namespace dt
+
 using namespace dt;
 
 extern "C" {
 
 size_t dt_paged_attn_workspace_bytes(int batch, int total_rows, int Hq, int Hkv, int d) {
   if (batch < 1 || total_rows < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || d < 1) return 0;
-  return paged_workspace(total_rows, Hq, Hkv, d);
+  return paged_workspace((int64_t)total_rows * (Hq / Hkv), d);
 }
 
 dt_status dt_paged_attn(const void* d_q, int64_t ld_q, const int32_t* d_row_start,
@@ -171,7 +215,7 @@ dt_status dt_paged_attn(const void* d_q, int64_t ld_q, const int32_t* d_row_star
   if (!d_row_start || !d_kv_len || total_rows < 0 || max_rows < 1) return DT_EINVAL;
   if (ld_q < (int64_t)Hq * cache->d || (ld_q * (dt == DT_F32 ? 4 : 2)) % 16) return DT_EINVAL;
   if ((int64_t)total_rows * Hq >= (int64_t)1 << 30) return DT_EUNSUPPORTED;
-  if (!ws || ws_bytes < paged_workspace(total_rows, Hq, cache->Hkv, cache->d))
+  if (!ws || ws_bytes < paged_workspace((int64_t)total_rows * (Hq / cache->Hkv), cache->d))
     return DT_EWORKSPACE;
   PagedArgs a = {};
   a.q = d_q;
@@ -190,12 +234,12 @@ dt_status dt_paged_attn(const void* d_q, int64_t ld_q, const int32_t* d_row_star
   a.n_sink = n_sink;
   a.out = d_out;
   a.status = (int32_t*)ws;
-  return run_paged(a, cache->dt, dt, (cudaStream_t)stream);
+  return run_paged(a, cache, dt, ws, (cudaStream_t)stream);
 }
 
 size_t dt_tree_verify_attn_paged_workspace_bytes(int batch, int Nmax, int Hq, int Hkv, int d) {
   if (batch < 1 || Nmax < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || d < 1) return 0;
-  return paged_workspace((int64_t)batch * (Nmax + 1), Hq, Hkv, d);
+  return paged_workspace((int64_t)(Nmax + 1) * (Hq / Hkv), d);
 }
 
 dt_status dt_tree_verify_attn_paged(const void* d_q, const dt_kv_cache* cache,
@@ -217,7 +261,7 @@ dt_status dt_tree_verify_attn_paged(const void* d_q, const dt_kv_cache* cache,
   if (Nmax > 64 || (window && window <= Nmax)) return DT_EUNSUPPORTED;
   const int rows = batch * (Nmax + 1);
   if ((int64_t)rows * Hq >= (int64_t)1 << 30) return DT_EUNSUPPORTED;
-  if (!ws || ws_bytes < paged_workspace(rows, Hq, cache->Hkv, cache->d)) return DT_EWORKSPACE;
+  if (!ws || ws_bytes < paged_workspace((int64_t)(Nmax + 1) * (Hq / cache->Hkv), cache->d)) return DT_EWORKSPACE;
   PagedArgs a = {};
   a.q = d_q;
   a.ld_q = (int64_t)Hq * cache->d;
@@ -240,7 +284,7 @@ dt_status dt_tree_verify_attn_paged(const void* d_q, const dt_kv_cache* cache,
   a.Nmax = Nmax;
   a.out = d_out;
   a.status = (int32_t*)ws;
-  return run_paged(a, cache->dt, dt, (cudaStream_t)stream);
+  return run_paged(a, cache, dt, ws, (cudaStream_t)stream);
 }
 
 }  // extern "C"
