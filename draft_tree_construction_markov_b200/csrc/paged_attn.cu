@@ -33,10 +33,39 @@ __global__ void __launch_bounds__(32 * kPlainWarps) paged_plain_kernel(PagedArgs
 // a warp takes a row, its lanes four columns each.
 constexpr int kJoinWarps = 8, kJoinRows = 32;
 
+// Rows that worker blockIdx.x finished and that came out infinite or NaN: again,
+// key by key (see paged_row).
+template <int CT>
+__device__ __noinline__ void join_redo(const PagedArgs& a, Cut cut) {
+  __shared__ int64_t sums[kMaxKvBatch + 1];
+  const int64_t all = count_units(a, sums, cut);
+  const int workers = (int)min((int64_t)gridDim.x, all), me = blockIdx.x;
+  if (me >= workers) return;
+  const int64_t u0 = first_unit(all, me, workers);
+  int64_t left = first_unit(all, me + 1, workers) - u0;
+  const int lane = threadIdx.x & 31;
+  Cursor c;
+  for (c.seek(a, sums, u0, cut);; c.next_tile(a, cut)) {
+    if (c.u == 0 && c.t.units <= left) {
+      for (int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+           r < min(c.t.live, (int)(blockIdx.y + 1) * kJoinRows); r += kJoinWarps) {
+        const int i = (c.t.m0 + r) / a.G, h = c.kvh * a.G + (c.t.m0 + r) % a.G;
+        const uint16_t* out = (const uint16_t*)a.out + (((int64_t)c.rq.r0 + i) * a.Hq + h) * a.d;
+        bool odd = false;
+        for (int e = lane; e < a.d; e += 32) odd |= (out[e] & 0x7f80u) == 0x7f80u;
+        if (__any_sync(0xffffffffu, odd)) paged_row<CT, DT_BF16>(a, c.b, i, h);
+      }
+    }
+    left -= c.t.units - c.u;
+    if (left <= 0) break;
+  }
+}
+
 template <int CT>
 __global__ void __launch_bounds__(32 * kJoinWarps)
     paged_join_kernel(const __grid_constant__ PagedArgs a, Cut cut) {
   pdl_wait();
+  if (a.redo[blockIdx.x]) join_redo<CT>(a, cut);
   const PagedSplit sp = a.split[blockIdx.x];
   if (sp.parts == 0) return;
   const PagedRequest rq = paged_request(a, sp.b);
@@ -105,11 +134,12 @@ EncodeFn encode_fn() {
 // Records, fp32 sums and statistics of the row tiles that shares cut, two per
 // worker; `all`: (row, head) pairs of a KV head that a row tile can have at most.
 struct PartPlan {
-  size_t sums, stats, bytes;  // offsets behind the header, and all
+  size_t redo, sums, stats, bytes;  // offsets behind the header, and all
 };
 PartPlan part_plan(int64_t workers, int64_t rows, int d) {
   PartPlan p;
-  p.sums = workers * sizeof(PagedSplit);
+  p.redo = workers * sizeof(PagedSplit);
+  p.sums = p.redo + ((workers * 4 + 15) & ~(size_t)15);
   p.stats = p.sums + 2 * workers * rows * d * 4;
   p.bytes = kWsHeader + p.stats + 2 * workers * rows * sizeof(float2);
   return p;
@@ -146,6 +176,7 @@ dt_status run_paged(PagedArgs a, const dt_kv_cache* cache, int dt, void* ws, cud
   const PartPlan p = part_plan(few ? kDecodeWorkers : 2 * kPagedSms / tiles, a.part_rows, a.d);
   uint8_t* w = (uint8_t*)ws + kWsHeader;
   a.split = (PagedSplit*)w;
+  a.redo = (int*)(w + p.redo);
   a.part_o = (float*)(w + p.sums);
   a.part_ml = (float2*)(w + p.stats);
   const cudaError_t e = few ? launch_paged_decode(a, ct, cache, (int)pairs, s)

@@ -29,6 +29,7 @@ struct PagedArgs {
   int32_t* status;
   // split-and-join workspace (PagedSplit)
   struct PagedSplit* split;
+  int* redo;        // [workers]: some finished row came out infinite or NaN
   float2* part_ml;  // [2 * workers][part_rows]: (max in log2 units, sum)
   float* part_o;    // [2 * workers][part_rows][d], not yet divided by the sum
   int part_rows;

@@ -163,7 +163,10 @@ __global__ void __launch_bounds__(DecShape<D, CT, NT>::kThreads, 1)
   uint64_t* empty = full + ST;
   uint8_t* my_ring = ring + w * ST * S::kStage;
   float* my_scales = scales + w * ST * 2 * KEYS;
-  if (warp < kDecWarps && lane == 0 && !busy) a.split[me].parts = 0;
+  if (warp < kDecWarps && lane == 0) {
+    a.redo[me] = 0;
+    if (!busy) a.split[me].parts = 0;
+  }
 
   if (warp == kDecWarps) {
     // ------------------------------------- the loader: lane w fills worker w's ring

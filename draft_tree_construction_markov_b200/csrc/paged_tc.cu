@@ -25,6 +25,7 @@
 // CTAs in equal consecutive shares; a row tile that two shares cut is joined by
 // paged_join_kernel from fp32 partials.
 #include <algorithm>
+#include <type_traits>
 
 #include "paged_attn.cuh"
 
@@ -73,17 +74,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr));
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31]), "r"(taddr)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
@@ -100,6 +90,35 @@ __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Two fp32 operations an instruction.
+__device__ __forceinline__ void mul2(uint32_t& x, uint32_t& y, float f, float g) {
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n"
+      " mul.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "+r"(x), "+r"(y)
+      : "f"(f), "f"(g));
+}
+__device__ __forceinline__ void fma2(uint32_t x, uint32_t y, float f, float g, float& u, float& v) {
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %4};\n"
+      " mov.b64 c, {%5, %5};\n fma.rn.f32x2 a, a, b, c;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "=f"(u), "=f"(v)
+      : "r"(x), "r"(y), "f"(f), "f"(g));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float f, float g) {
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n"
+      " add.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "+f"(x), "+f"(y)
+      : "f"(f), "f"(g));
+}
+
+// A warpgroup goes from `from` registers a thread to `to`.
+template <int from, int to>
+__device__ __forceinline__ void deal_regs() {
+  if constexpr (to > from)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(to));
+  else if constexpr (to < from)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(to));
+}
+
 template <int D, int CT, int NQ>
 struct TcShape {
   static constexpr bool kTma = CT == DT_BF16;
@@ -109,15 +128,34 @@ struct TcShape {
   // key tiles in flight: a second one where shared memory has room for it
   static constexpr int kStages = NQ == 2 || D == 64 ? 2 : 1;
   static constexpr int kScales = 4;             // tiles of row scales (see the loader)
+  // 32-column parts of S that a row keeps in registers between its two passes
+  static constexpr int kKeep = NQ == 2 && kTma ? 4 : 2;
+  // Where shared memory or conversion leaves few registers, the warps come in
+  // whole warpgroups and deal them out anew: more for the softmax (S in
+  // registers), less for the others.  (A function call in the kernel would
+  // undo this: the compiler then allots the least of them to all.)
+  static constexpr bool kDeal = NQ == 2 || !kTma;
+  static constexpr int kSoftRegs = kTma ? 200 : NQ == 2 ? 152 : 104;
+  static constexpr int kLoadRegs = kTma ? 104 : NQ == 2 ? 112 : 88;
+  static constexpr int kMmaRegs = kTma ? kLoadRegs : NQ == 2 ? 88 : 48;
+  // registers a thread at launch (the most that the launch bounds leave), and
+  // that the shares add up to no more
+  static constexpr int kLaunchRegs = NQ == 1 ? 80 : kTma ? 168 : 128;
+  static_assert(NQ == 2 ? (kTma ? 2 * kSoftRegs + kLoadRegs <= 3 * kLaunchRegs
+                                : 2 * kSoftRegs + kLoadRegs + kMmaRegs <= 4 * kLaunchRegs)
+                        : kTma || kSoftRegs + kLoadRegs + kMmaRegs <= 3 * kLaunchRegs);
   static constexpr int kSoft = 128 * NQ;
-  static constexpr int kLoad = kTma ? 32 : 128;
-  static constexpr int kThreads = kSoft + 32 + kLoad;
+  // (a TMA loader and the MMAs share a warpgroup)
+  static constexpr int kMma = kDeal && !kTma ? 128 : 32;
+  static constexpr int kLoad = !kTma ? 128 : kDeal ? 96 : 32;
+  static constexpr int kThreads = kSoft + kMma + kLoad;
   static constexpr int kPerSm = NQ == 2 ? 1 : 2;
   static constexpr uint32_t kTmemCols = NQ == 2 ? 512 : 256;  // S: 128 columns a row tile, O: D
   static constexpr int kRows = 128 * NQ;
   static constexpr int kBars = 4 * kStages + 4 * NQ + kScales;
   static constexpr size_t kSmem = (size_t)(NQ + 2 * kStages) * kOperand +
-                                  (kTma ? 0 : kScales * 2 * 128 * 4) + kBars * 8 + 32 + 1024;
+                                  (kTma ? 0 : kScales * (3 * 128 * 4 + 16)) + kBars * 8 + 16 + kThreads / 32 * sizeof(Cursor) + 1024;
+  static_assert(sizeof(Cursor) % 8 == 0);
 };
 
 struct TcMaps {
@@ -153,7 +191,9 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
   uint8_t* sk = sq + NQ * S::kOperand;             // K [ST][KC][128 keys][128 B]
   uint8_t* sv = sk + ST * S::kOperand;             // V [ST][KC][128 keys][128 B]
   float* sscale = (float*)(sv + ST * S::kOperand); // [kScales][K, V][128]
-  uint64_t* bars = (uint64_t*)((uint8_t*)sscale + (S::kTma ? 0 : S::kScales * 2 * 128 * 4));
+  int4* sinfo = (int4*)(sscale + (S::kTma ? 0 : S::kScales * 2 * 128));  // [kScales]
+  int* sslot = (int*)(sinfo + (S::kTma ? 0 : S::kScales));               // [kScales][128]
+  uint64_t* bars = (uint64_t*)(sslot + (S::kTma ? 0 : S::kScales * 128));
   uint64_t* k_full = bars;
   uint64_t* k_empty = k_full + ST;
   uint64_t* v_full = k_empty + ST;
@@ -165,12 +205,14 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
   uint64_t* c_full = o_full + NQ;                  // the scales of a tile are there
   uint32_t* tslot = (uint32_t*)(c_full + S::kScales);
   volatile int* abort_flag = (volatile int*)(tslot + 1);
-  int64_t* sums = (int64_t*)(tslot + 4);           // [batch + 1]
+  Cursor* cursors = (Cursor*)(tslot + 4);          // [warps]
+  int64_t* sums = (int64_t*)(cursors + S::kThreads / 32);  // [batch + 1]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  Cursor& c = cursors[warp];
   constexpr Cut cut = {S::kRows, 7};
   static_assert(kTcKeys == 1 << 7);
-  constexpr int kWarpMma = 4 * NQ, kWarpLoad = kWarpMma + 1;
+  constexpr int kWarpMma = 4 * NQ, kWarpLoad = kWarpMma + S::kMma / 32;
   pdl_launch_dependents();  // the join may be scheduled (it waits for this grid)
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
@@ -187,6 +229,7 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
     }
     for (int i = 0; i < S::kScales; ++i) mbar_init(&c_full[i], 128);
     *abort_flag = 0;
+    a.redo[blockIdx.x] = 0;
     fence_barrier_init();
   }
   if (warp == kWarpMma) {
@@ -203,15 +246,29 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return mbar_wait(bar, parity, a.status, abort_flag);
   };
+  auto seek = [&] {
+    if (lane == 0) c.seek(a, sums, u0, cut);
+    __syncwarp();
+  };
+  auto step = [&] {  // a whole warp: the next unit
+    __syncwarp();
+    if (lane == 0 && ++c.u == c.t.units) c.next_tile(a, cut);
+    __syncwarp();
+  };
 
-  if (left == 0) {
-    // nothing to do: fall through to the end
-  } else if (warp == kWarpMma) {
+  // The deal stands in each role's own branch, where the compiler allots by it,
+  // and every warp takes part in it, with work or without: a share is raised
+  // once the others have been lowered.
+  if (warp >= kWarpMma) {
+   if constexpr (S::kDeal && S::kTma)
+     deal_regs<S::kLaunchRegs, S::kLoadRegs>();
+   if (warp < kWarpLoad) {
     // ------------------------------------------------------------ the MMAs
-    if (lane == 0) {
+    if constexpr (S::kDeal && !S::kTma)
+      deal_regs<S::kLaunchRegs, S::kMmaRegs>();
+    if (warp == kWarpMma && lane == 0 && left > 0) {
       constexpr uint32_t is = idesc_bf16_f32(128, 128);
       constexpr uint32_t io = idesc_bf16_f32(128, D) | (1u << 16);  // B is MN-major
-      Cursor c;
       c.seek(a, sums, u0, cut);
       record_split(a, c, all, cta, shares);
       int ns = 0, np = 0;                // key tiles whose S / O was issued
@@ -286,11 +343,13 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
         first = first_next;
       }
     }
-  } else if (warp >= kWarpLoad) {
+   } else {
     // ------------------------------------------------------------ the loads
-    Cursor c;
-    c.seek(a, sums, u0, cut);
+    if constexpr (S::kDeal && !S::kTma)
+      deal_regs<S::kLaunchRegs, S::kLoadRegs>();
+    if (left > 0 && (!S::kTma || warp == kWarpLoad)) {
     bool ok = true;
+    seek();
     if constexpr (S::kTma) {
       const int page = 1 << a.c.page_shift, box = min(page, 128);
       for (int g = 0; left > 0 && ok; ++g, --left) {
@@ -325,124 +384,153 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
         load(&maps.k, &maps.kt, sk + st * S::kOperand, &k_full[st], &k_empty[st]);
         __syncwarp();
         load(&maps.v, &maps.vt, sv + st * S::kOperand, &v_full[st], &v_empty[st]);
-        __syncwarp();
-        if (left > 1 && ++c.u == c.t.units) c.next_tile(a, cut);
+        if (left > 1) step();
       }
     } else {
-      // 8-bit codes: a thread takes every 128th 16-byte piece of the tile
+      // 8-bit codes: a thread takes every 128th 16-byte piece of the tile.  The
+      // slots of a tile's positions (one a thread) are looked up two tiles ahead,
+      // its codes are in registers one tile ahead.
       constexpr int kRowPieces = D / 16, kPieces = 128 * kRowPieces / 128;
       const int lt = tid - kWarpLoad * 32;
-      const int piece = lt % kRowPieces;
+      const int piece = lt % kRowPieces, row0 = lt / kRowPieces;
       uint4 kw[kPieces], vw[kPieces];
       float kscale = 0.f, vscale = 0.f;
-      // slot of the tile's position j for this KV head, or -1
-      auto slot_of = [&](int base, int j) -> int64_t {
-        const int s = base + j;
-        if (!piece_seen(c.t, s, 1)) return -1;
+      // this thread's slot of the tile at the cursor, -1: read as zeros
+      auto look_up = [&]() -> int {
+        const int s = unit_base(a, c.t, c.u, cut) + lt;
+        if (s < lt || !piece_seen(c.t, s, 1)) return -1;
         const int64_t slot = a.c.slot(c.b, s, a.status);
-        return slot < 0 ? -1 : slot + ((int64_t)c.kvh << a.c.page_shift);
+        return slot < 0 ? -1 : (int)(slot + ((int64_t)c.kvh << a.c.page_shift));
       };
-      auto fetch = [&](const void* cache, const float* scales, uint4 (&w)[kPieces], float& scale) {
-        const int base = unit_base(a, c.t, c.u, cut);
-        if (base < 0) return;
+      auto plan = [&](int g, int slot) {
+        sslot[(g % S::kScales) * 128 + lt] = slot;
+        if (lt == 0)
+          sinfo[g % S::kScales] = make_int4(unit_base(a, c.t, c.u, cut), c.kvh, c.rq.r0, c.rq.n);
+      };
+      auto sync = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+      auto fetch = [&](int g, const void* cache, const float* scales, uint4 (&w)[kPieces],
+                       float& scale) {
+        if (sinfo[g % S::kScales].x < 0) return;
+        const int* slots = sslot + (g % S::kScales) * 128;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-          const int64_t slot = slot_of(base, (lt + i * 128) / kRowPieces);
-          w[i] = slot < 0 ? make_uint4(0, 0, 0, 0)
-                          : __ldg((const uint4*)((const uint8_t*)cache + slot * D + piece * 16));
+          const int slot = slots[row0 + i * (128 / kRowPieces)];
+          w[i] = make_uint4(0, 0, 0, 0);
+          if (slot >= 0)
+            w[i] = __ldg((const uint4*)((const uint8_t*)cache + (int64_t)slot * D + piece * 16));
         }
-        const int64_t slot = slot_of(base, lt);
+        const int slot = slots[lt];
         scale = slot < 0 ? 0.f : __ldg(scales + slot);
       };
       // the tile into shared memory as bf16: codes that are in registers, or the tree's rows
-      auto place = [&](uint8_t* dst, const void* tree, const uint4 (&w)[kPieces]) {
-        if (unit_base(a, c.t, c.u, cut) < 0) {
+      auto place = [&](int g, uint8_t* dst, const void* tree, const uint4 (&w)[kPieces]) {
+        const int4 info = sinfo[g % S::kScales];
+        if (info.x < 0) {
           const uint16_t* rows = (const uint16_t*)tree;
           for (int x = lt; x < 128 * KC * 8; x += 128) {
             const int cc = x % (KC * 8), r = x / (KC * 8);
             uint4 v = make_uint4(0, 0, 0, 0);
-            if (r < c.rq.n)
-              v = *(const uint4*)(rows + (((int64_t)c.rq.r0 + r) * a.c.Hkv + c.kvh) * D + cc * 8);
+            if (r < info.w)
+              v = *(const uint4*)(rows + (((int64_t)info.z + r) * a.c.Hkv + info.y) * D + cc * 8);
             *(uint4*)(dst + (cc >> 3) * S::kChunk + sw128(r, cc & 7)) = v;
           }
           return;
         }
+        uint8_t* at = dst + (piece >> 2) * S::kChunk;
+        // the lanes of the second 64 columns store their halves in the other order: all 32 banks
+        const int c0 = (piece & 3) * 2, odd = piece >> 2;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-          const int r = (lt + i * 128) / kRowPieces;
+          const int r = row0 + i * (128 / kRowPieces);
           uint32_t o[8];
           const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) codes_to_bf16<CT>(in[e], o[2 * e], o[2 * e + 1]);
-          uint8_t* at = dst + (piece >> 2) * S::kChunk;
-          const int c0 = (piece & 3) * 2;
-          // the lanes of the second 64 columns store their halves in the other order: all 32 banks
-          const int odd = piece >> 2;
           *(uint4*)(at + sw128(r, c0 + odd)) =
               odd ? make_uint4(o[4], o[5], o[6], o[7]) : make_uint4(o[0], o[1], o[2], o[3]);
           *(uint4*)(at + sw128(r, c0 + 1 - odd)) =
               odd ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(o[4], o[5], o[6], o[7]);
         }
       };
-      fetch(a.c.k, a.c.ks, kw, kscale);
-      fetch(a.c.v, a.c.vs, vw, vscale);
+      plan(0, look_up());
+      if (left > 1) {
+        step();
+        plan(1, look_up());
+      }
+      sync();
+      fetch(0, a.c.k, a.c.ks, kw, kscale);
+      fetch(0, a.c.v, a.c.vs, vw, vscale);
       for (int g = 0; left > 0; ++g, --left) {
         const int st = g % ST;
         const uint32_t parity = ((g / ST) & 1) ^ 1;
-        const bool tree = unit_base(a, c.t, c.u, cut) < 0;
+        int ahead = -1;
+        if (left > 2) {
+          step();
+          ahead = look_up();
+        }
         // The scales' slot was last used by tile g - 4.  k_empty means that S of
         // tile g - ST is complete, which was issued only after the softmax of
         // the tile before it had handed over P; so tile g - ST - 1 >= g - 4 is done.
         float* scales = sscale + (g % S::kScales) * 256;
-        Cursor now = c;
-        ok = ok && wait(&k_empty[st], parity);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        place(sk + st * S::kOperand, a.kt, kw);
-        scales[lt] = tree ? 1.f : kscale;
-        scales[128 + lt] = tree ? 1.f : vscale;
-        fence_async_smem();
-        mbar_arrive(&k_full[st]);
-        mbar_arrive(&c_full[g % S::kScales]);
-        // the next tile's loads are on their way while this one is worked on
-        bool more = left > 1;
-        if (more && ++c.u == c.t.units) c.next_tile(a, cut);
-        if (more) fetch(a.c.k, a.c.ks, kw, kscale);
-        Cursor next = c;
-        c = now;
-        ok = wait(&v_empty[st], parity);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        place(sv + st * S::kOperand, a.vt, vw);
-        fence_async_smem();
-        mbar_arrive(&v_full[st]);
-        c = next;
-        if (more) fetch(a.c.v, a.c.vs, vw, vscale);
+        // (a warp that gives up goes on to the barriers, so that the others pass them)
+        ok = __all_sync(0xffffffffu, ok && wait(&k_empty[st], parity));
+        if (ok) {
+          place(g, sk + st * S::kOperand, a.kt, kw);
+          const bool tree = sinfo[g % S::kScales].x < 0;
+          scales[lt] = tree ? 1.f : kscale;
+          scales[128 + lt] = tree ? 1.f : vscale;
+          fence_async_smem();
+          mbar_arrive(&k_full[st]);
+          mbar_arrive(&c_full[g % S::kScales]);
+          // the next tile's loads are on their way while this one is worked on
+          if (left > 1) fetch(g + 1, a.c.k, a.c.ks, kw, kscale);
+          ok = __all_sync(0xffffffffu, wait(&v_empty[st], parity));
+        }
+        if (ok) {
+          place(g, sv + st * S::kOperand, a.vt, vw);
+          fence_async_smem();
+          mbar_arrive(&v_full[st]);
+          if (left > 1) fetch(g + 1, a.c.v, a.c.vs, vw, vscale);
+        }
+        if (left > 2) plan(g + 2, ahead);
+        sync();
       }
     }
+   }
+   }
   } else {
     // ---------------------------------------------------------- the softmax
+    if constexpr (S::kDeal) deal_regs<S::kLaunchRegs, S::kSoftRegs>();
+   if (left > 0) {
     const int q = warp >> 2, row = tid & 127;
     const uint32_t quad = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + quad + q * 128, to = tmem + quad + NQ * 128 + q * D;
     uint8_t* my_q = sq + q * S::kOperand;
     const float sl2 = a.scale * kL2e;
-    Cursor c;
-    c.seek(a, sums, u0, cut);
+    seek();
+    auto next_tile = [&] {
+      __syncwarp();
+      if (lane == 0) c.next_tile(a, cut);
+      __syncwarp();
+    };
     // the row tile's queries into shared memory, zeros where there is no row
-    auto load_q = [&](const Cursor& c) {
+    auto load_q = [&] {
+      const int m0 = c.t.m0 + q * 128, live = c.t.live - q * 128, r0 = c.rq.r0, h0 = c.kvh * a.G;
+#pragma unroll 4
       for (int x = row; x < 128 * KC * 8; x += 128) {
         const int cc = x % (KC * 8), r = x / (KC * 8);
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (q * 128 + r < c.t.live) {
-          const int m = c.t.m0 + q * 128 + r;
-          v = *(const uint4*)((const uint16_t*)a.q + (c.rq.r0 + (int64_t)(m / a.G)) * a.ld_q +
-                              ((int64_t)c.kvh * a.G + m % a.G) * D + cc * 8);
+        if (r < live) {
+          const int m = m0 + r;
+          v = *(const uint4*)((const uint16_t*)a.q + (r0 + (int64_t)(m / a.G)) * a.ld_q +
+                              ((int64_t)h0 + m % a.G) * D + cc * 8);
         }
         *(uint4*)(my_q + (cc >> 3) * S::kChunk + sw128(r, cc & 7)) = v;
       }
       fence_async_smem();
       mbar_arrive(&q_full[q]);
     };
-    if (q * 128 < c.t.live) load_q(c);
+    if (q * 128 < c.t.live) load_q();
     bool ok = true;
     int n_done = 0;  // key tiles of this row tile's barriers
     int g = 0;       // key tiles of the CTA
@@ -454,8 +542,8 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
         left -= seg;
         head = false;
         if (left > 0) {
-          c.next_tile(a, cut);
-          if (q * 128 < c.t.live) load_q(c);
+          next_tile();
+          if (q * 128 < c.t.live) load_q();
         }
         continue;
       }
@@ -490,90 +578,113 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
           break;
         }
         tc_fence_after();
-        // ---- the row's largest score of this tile
-        float top = -INFINITY;
-        uint32_t r[32];
+        auto tile = [&](auto masked_c) -> bool {
+          constexpr bool kMasked = decltype(masked_c)::value;
+          constexpr int kKeep = S::kKeep;
+          // ---- the row's largest score of this tile
+          uint32_t r[kKeep][32];
+          auto load = [&](int w) { tmem_ld32(ts + 32 * w, r[w % kKeep]); };
+          // scores of part w: times the keys' scales, -infinity where the row does not see
+          auto finish = [&](int w) {
+            const uint32_t see = kMasked ? mask.word(base, w) : 0;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          tmem_ld32(ts + 32 * w, r);
-          tmem_wait_ld();
-          const uint32_t see = masked ? mask.word(base, w) : 0xffffffffu;
-          float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            float4 sc = make_float4(1.f, 1.f, 1.f, 1.f);
-            if constexpr (!S::kTma) sc = *(const float4*)(scales + 32 * w + e);
-            const float f[4] = {sc.x, sc.y, sc.z, sc.w};
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              float s = __uint_as_float(r[e + x]);
-              if constexpr (!S::kTma) s *= f[x];
-              if (masked) s = (see >> (e + x)) & 1u ? s : -INFINITY;
-              t4[x] = fmaxf(t4[x], s);
-            }
-          }
-          top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])));
-        }
-        top *= sl2;
-        // ---- the maximum in use
-        if (k == 0) {
-          m = top;
-        } else if (__any_sync(0xffffffffu, top > m + kRescale)) {
-          const float now = fmaxf(m, top);
-          const float keep = m == now ? 1.f : ex2(m - now);
-          l *= keep;
-          m = now;
-          ok = wait(&o_full[q], (n_done - 1) & 1);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-#pragma unroll
-          for (int w = 0; w < D / 32; ++w) {
-            tmem_ld32(to + 32 * w, r);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * keep);
-            tmem_st32(to + 32 * w, r);
-          }
-        }
-        const float use = m == -INFINITY ? 0.f : m;
-        // ---- weights, in bf16 for the second product, over the scores
-        float l4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          tmem_ld32(ts + 32 * w, r);
-          tmem_wait_ld();
-          const uint32_t see = masked ? mask.word(base, w) : 0xffffffffu;
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            float4 sc = make_float4(1.f, 1.f, 1.f, 1.f), vc = sc;
-            if constexpr (!S::kTma) {
-              sc = *(const float4*)(scales + 32 * w + e);
-              vc = *(const float4*)(scales + 128 + 32 * w + e);
-            }
-            const float f[4] = {sc.x, sc.y, sc.z, sc.w}, fv[4] = {vc.x, vc.y, vc.z, vc.w};
-            float p[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              float s = __uint_as_float(r[e + x]);
-              if constexpr (!S::kTma) s *= f[x];
-              p[x] = ex2(fmaf(s, sl2, -use));
-              if (masked) p[x] = (see >> (e + x)) & 1u ? p[x] : 0.f;
-              l4[x] += p[x];
+            for (int e = 0; e < 32; e += 4) {
+              uint32_t* x = r[w % kKeep] + e;
               if constexpr (!S::kTma) {
-                p[x] *= fv[x];
-                if (masked) p[x] = (see >> (e + x)) & 1u ? p[x] : 0.f;
+                const float4 f = *(const float4*)(scales + 32 * w + e);
+                mul2(x[0], x[1], f.x, f.y);
+                mul2(x[2], x[3], f.z, f.w);
+              }
+              if constexpr (kMasked) {
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                  x[y] = (see >> (e + y)) & 1u ? x[y] : 0xff800000u;
               }
             }
-            pk[e / 2] = pack2(p[0], p[1]);
-            pk[e / 2 + 1] = pack2(p[2], p[3]);
+          };
+          float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          // the first parts are read twice where not all of them fit the registers
+#pragma unroll
+          for (int w0 = 4 - kKeep; w0 >= 0; w0 -= kKeep) {
+#pragma unroll
+            for (int w = w0; w < w0 + kKeep; ++w) load(w);
+            tmem_wait_ld();
+#pragma unroll
+            for (int w = w0; w < w0 + kKeep; ++w) {
+              finish(w);
+#pragma unroll
+              for (int e = 0; e < 32; e += 2)
+                t4[(e / 2) % 4] = fmaxf(fmaxf(t4[(e / 2) % 4], __uint_as_float(r[w % kKeep][e])),
+                                        __uint_as_float(r[w % kKeep][e + 1]));
+            }
           }
-          tmem_st16(ts + 16 * w, pk);
-        }
-        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+          const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * sl2;
+          // ---- the maximum in use
+          if (k == 0) {
+            m = top;
+          } else if (__any_sync(0xffffffffu, top > m + kRescale)) {
+            const float now = fmaxf(m, top);
+            const float keep = m == now ? 1.f : ex2(m - now);
+            l *= keep;
+            m = now;
+            if (!__all_sync(0xffffffffu, wait(&o_full[q], (n_done - 1) & 1))) return false;
+            tc_fence_after();
+            uint32_t x[16];
+#pragma unroll
+            for (int w = 0; w < D / 16; ++w) {
+              tmem_ld16_nowait(to + 16 * w, x);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * keep);
+              tmem_st16(to + 16 * w, x);
+            }
+          }
+          const float less = m == -INFINITY ? 0.f : -m;
+          // ---- weights, in bf16 for the second product, over the scores
+          float la[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            if (w >= kKeep && w % kKeep == 0) {
+#pragma unroll
+              for (int x = w; x < w + kKeep; ++x) load(x);
+              tmem_wait_ld();
+#pragma unroll
+              for (int x = w; x < w + kKeep; ++x) finish(x);
+            }
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              uint32_t* x = r[w % kKeep] + e;
+              float p[4];
+              fma2(x[0], x[1], sl2, less, p[0], p[1]);
+              fma2(x[2], x[3], sl2, less, p[2], p[3]);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) p[y] = ex2(p[y]);
+              add2(la[0], la[1], p[0], p[1]);
+              add2(la[2], la[3], p[2], p[3]);
+              if constexpr (!S::kTma) {
+                const float4 f = *(const float4*)(scales + 128 + 32 * w + e);
+                uint32_t z[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) z[y] = __float_as_uint(p[y]);
+                mul2(z[0], z[1], f.x, f.y);
+                mul2(z[2], z[3], f.z, f.w);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                  // (a scale of a place that the row does not see may be NaN)
+                  p[y] = kMasked && x[y] == 0xff800000u ? 0.f : __uint_as_float(z[y]);
+                }
+              }
+              pk[e / 2] = pack2(p[0], p[1]);
+              pk[e / 2 + 1] = pack2(p[2], p[3]);
+            }
+            tmem_st16(ts + 16 * w, pk);
+          }
+          l += (la[0] + la[1]) + (la[2] + la[3]);
+          return true;
+        };
+        ok = masked ? tile(std::true_type()) : tile(std::false_type());
+        if (!ok) break;
         if constexpr (S::kTma) {
           // V rows that are no positions of the request may hold anything: zeros, before 0 * NaN
           const int valid = base < 0 ? c.rq.n : c.rq.len - base;
@@ -599,10 +710,10 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
       if (!ok) break;
       left -= seg;
       const bool whole = c.u == 0 && seg == c.t.units;
-      const Cursor now = c;
+      const int r0 = c.rq.r0;
       if (left > 0) {
-        c.next_tile(a, cut);
-        if (q * 128 < c.t.live) load_q(c);
+        next_tile();
+        if (q * 128 < c.t.live) load_q();
       }
       ok = __all_sync(0xffffffffu, wait(&o_full[q], (n_done - 1) & 1));
       if (!ok) break;
@@ -610,7 +721,7 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
       if (whole) {
         const bool sees = a.kt || mask.vis.sink > 0 || mask.vis.last > mask.vis.first;
         const float inv = row_factor(l, sees);
-        uint16_t* out = (uint16_t*)a.out + (((int64_t)now.rq.r0 + i) * a.Hq + h) * D;
+        uint16_t* out = (uint16_t*)a.out + (((int64_t)r0 + i) * a.Hq + h) * D;
         float odd = 0.f;  // NaN once an output is infinite or NaN
         uint32_t r[32];
 #pragma unroll
@@ -630,13 +741,8 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
             for (int e = 0; e < 4; ++e) *(uint4*)(out + 32 * w + 8 * e) = pk[e];
           }
         }
-        // finite weights, but not their sums with the values
-        unsigned again = __ballot_sync(0xffffffffu, there && sees && odd != 0.f && l - l == 0.f);
-        for (; again; again &= again - 1) {
-          const int from = __ffs(again) - 1;
-          paged_row<CT, DT_BF16>(a, now.b, __shfl_sync(0xffffffffu, i, from),
-                                 __shfl_sync(0xffffffffu, h, from));
-        }
+        // finite weights, but not their sums with the values: the join looks at them again
+        if (there && sees && odd != 0.f && l - l == 0.f) a.redo[cta] = 1;
       } else {
         const int64_t at = (int64_t)(2 * cta + (head ? 0 : 1)) * a.part_rows + q * 128 + row;
         float* po = a.part_o + at * D;
@@ -656,6 +762,7 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
       tc_fence_before();
       head = false;
     }
+   }
   }
   __syncwarp();
   if (*abort_flag) {
@@ -676,6 +783,14 @@ cudaError_t launch_shape(const PagedArgs& a, const TcMaps& maps, int ctas, cudaS
   using S = TcShape<D, CT, NQ>;
   const size_t smem = S::kSmem + 8 * ((size_t)a.batch + 1);
   auto kern = paged_tc_kernel<D, CT, NQ>;
+  if constexpr (S::kDeal) {
+    // the deal counts on the registers that a thread has at launch
+    static const bool as_compiled = [kern] {
+      cudaFuncAttributes f;
+      return cudaFuncGetAttributes(&f, kern) == cudaSuccess && f.numRegs == S::kLaunchRegs;
+    }();
+    if (!as_compiled) return cudaErrorInvalidKernelImage;
+  }
   // the limit is raised once, to the most that any batch needs
   cudaError_t e = ensure_smem(kern, S::kSmem + 8 * (kMaxKvBatch + 1));
   if (e != cudaSuccess) return e;
