@@ -24,6 +24,8 @@
 // The work of a call (row tiles x KV heads x key tiles) is divided over the
 // CTAs in equal consecutive shares; a row tile that two shares cut is joined by
 // paged_join_kernel from fp32 partials.
+#include <limits.h>
+
 #include <algorithm>
 #include <type_traits>
 
@@ -39,26 +41,35 @@ __device__ __forceinline__ uint32_t sw128(int r, int c) {
   return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4));
 }
 
-// Descriptor of an operand whose 64-element chunks of the M or N axis are
-// contiguous (128-byte-swizzled rows, one per K index): chunks `chunk` bytes
-// apart, 8-row groups 1024.
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t chunk) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFF);
-  d |= (uint64_t)((chunk >> 4) & 0x3FFF) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
+// Shared-memory descriptors by halves: only the address in the low one changes
+// from product to product.  K-major as in smem_desc_k_sw128; MN-major for an
+// operand whose 64-element chunks of the M or N axis are contiguous
+// (128-byte-swizzled rows, one per K index): chunks `chunk` bytes apart, 8-row
+// groups 1024.
+constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo_k(uint32_t saddr) {
+  return ((saddr >> 4) & 0x3FFF) | (1u << 16);
+}
+__device__ __forceinline__ uint32_t desc_lo_mn(uint32_t saddr, uint32_t chunk) {
+  return ((saddr >> 4) & 0x3FFF) | ((chunk >> 4) << 16);
 }
 
-// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                          uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A B, kind::f16, A from shared memory (ss) or TMEM (ts)
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n"
+      " mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
@@ -83,8 +94,37 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(taddr)
       : "memory");
 }
+// 16 rows x 64 columns, the layout of an mma.sync fragment: lane 4 i + j holds
+// columns 8 k + 2 j, 8 k + 2 j + 1 of row i in r[4 k], r[4 k + 1] and of row
+// i + 8 in r[4 k + 2], r[4 k + 3].
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// The same fragment as pairs of 16-bit values: r[2 k] row i, r[2 k + 1] row i + 8.
+__device__ __forceinline__ void tmem_st_frag16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(ok ? 16 : 0)
+               : "memory");
 }
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -119,6 +159,38 @@ __device__ __forceinline__ void deal_regs() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(to));
 }
 
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+// What a row sees, as bits over 32 neighbouring columns of a key tile.
+struct RowMask {
+  Visible vis;
+  uint32_t tree[3];  // tree rows 0..64
+  // columns [32 w, 32 w + 32) of the tile at position `base` (-1: the tree's)
+  __device__ __forceinline__ uint32_t word(int base, int w) const {
+    if (base < 0) return w == 0 ? tree[0] : w == 1 ? tree[1] : w == 2 ? tree[2] : 0u;
+    const int at = base + 32 * w;
+    return low_bits(vis.last - at) & (~low_bits(vis.first - at) | low_bits(vis.sink - at));
+  }
+};
+
+// A row tile's part of a CTA's share, as the schedule hands it to the other roles.
+struct Item {
+  int b, kvh, m0, live;       // request, KV head, (row, head) pairs [m0, m0 + live)
+  int r0, n, len, p0;         // PagedRequest
+  int u, seg, units, sinks;   // units [u, u + seg) of RowTile's
+  int first, lo, hi, sink;
+  __device__ __forceinline__ int base(const PagedArgs& a, int unit) const {
+    return unit < sinks ? unit * kTcKeys
+                        : a.kt && unit == units - 1 ? -1 : (first + unit - sinks) * kTcKeys;
+  }
+  __device__ __forceinline__ bool seen(int s, int count) const {
+    return (s < hi && s + count > lo) || s < sink;
+  }
+};
+static_assert(sizeof(Item) % 16 == 0);
+
 template <int D, int CT, int NQ>
 struct TcShape {
   static constexpr bool kTma = CT == DT_BF16;
@@ -128,8 +200,8 @@ struct TcShape {
   // key tiles in flight: a second one where shared memory has room for it
   static constexpr int kStages = NQ == 2 || D == 64 ? 2 : 1;
   static constexpr int kScales = 4;             // tiles of row scales (see the loader)
-  // 32-column parts of S that a row keeps in registers between its two passes
-  static constexpr int kKeep = NQ == 2 && kTma ? 4 : 2;
+  // 32-column parts of S that a row keeps in registers between its two passes (bf16 caches)
+  static constexpr int kKeep = NQ == 2 ? 4 : 2;
   // Where shared memory or conversion leaves few registers, the warps come in
   // whole warpgroups and deal them out anew: more for the softmax (S in
   // registers), less for the others.  (A function call in the kernel would
@@ -145,39 +217,24 @@ struct TcShape {
                                 : 2 * kSoftRegs + kLoadRegs + kMmaRegs <= 4 * kLaunchRegs)
                         : kTma || kSoftRegs + kLoadRegs + kMmaRegs <= 3 * kLaunchRegs);
   static constexpr int kSoft = 128 * NQ;
-  // (a TMA loader and the MMAs share a warpgroup)
-  static constexpr int kMma = kDeal && !kTma ? 128 : 32;
-  static constexpr int kLoad = !kTma ? 128 : kDeal ? 96 : 32;
+  // warps of the MMAs, of the schedule, of a TMA loader, and idle ones that fill a warpgroup;
+  // the loaders of codes are a warpgroup of their own
+  static constexpr int kMma = kDeal ? 128 : 96;
+  static constexpr int kLoad = kTma ? 0 : 128;
+  static constexpr int kLoadWarps = kTma ? 1 : 4;
   static constexpr int kThreads = kSoft + kMma + kLoad;
+  static constexpr int kItems = 4;  // row tiles that the schedule is ahead
   static constexpr int kPerSm = NQ == 2 ? 1 : 2;
   static constexpr uint32_t kTmemCols = NQ == 2 ? 512 : 256;  // S: 128 columns a row tile, O: D
   static constexpr int kRows = 128 * NQ;
-  static constexpr int kBars = 4 * kStages + 4 * NQ + kScales;
+  static constexpr int kBars = 4 * kStages + 4 * NQ + kScales + 2 * kItems;
   static constexpr size_t kSmem = (size_t)(NQ + 2 * kStages) * kOperand +
-                                  (kTma ? 0 : kScales * (3 * 128 * 4 + 16)) + kBars * 8 + 16 + kThreads / 32 * sizeof(Cursor) + 1024;
-  static_assert(sizeof(Cursor) % 8 == 0);
+                                  (kTma ? 0 : kScales * (3 * 128 * 4 + 16) + kSoft * sizeof(RowMask)) + kItems * sizeof(Item) + kBars * 8 + 16 + 1024;
 };
 
 struct TcMaps {
   CUtensorMap k, v;    // the cache, [slots][D], boxes of 64 x min(page, 128)
   CUtensorMap kt, vt;  // the tree's rows, [rows][Hkv * D], boxes of 64 x (Nmax + 1)
-};
-
-__device__ __forceinline__ uint32_t low_bits(int n) {
-  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
-}
-
-// What a row sees, as bits over 32 neighbouring columns of a key tile.
-struct RowMask {
-  Visible vis;
-  uint64_t tree;  // tree rows 0..63; row 64 in `top`
-  uint32_t top;
-  // columns [32 w, 32 w + 32) of the tile at position `base` (-1: the tree's)
-  __device__ __forceinline__ uint32_t word(int base, int w) const {
-    if (base < 0) return w == 0 ? (uint32_t)tree : w == 1 ? (uint32_t)(tree >> 32) : w == 2 ? top : 0u;
-    const int at = base + 32 * w;
-    return low_bits(vis.last - at) & (~low_bits(vis.first - at) | low_bits(vis.sink - at));
-  }
 };
 
 template <int D, int CT, int NQ>
@@ -190,10 +247,12 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
   uint8_t* sq = smem;                              // Q [NQ][KC][128 rows][128 B]
   uint8_t* sk = sq + NQ * S::kOperand;             // K [ST][KC][128 keys][128 B]
   uint8_t* sv = sk + ST * S::kOperand;             // V [ST][KC][128 keys][128 B]
-  float* sscale = (float*)(sv + ST * S::kOperand); // [kScales][K, V][128]
+  Item* items = (Item*)(sv + ST * S::kOperand);    // [kItems]
+  float* sscale = (float*)(items + S::kItems);     // [kScales][K, V][128]
   int4* sinfo = (int4*)(sscale + (S::kTma ? 0 : S::kScales * 2 * 128));  // [kScales]
   int* sslot = (int*)(sinfo + (S::kTma ? 0 : S::kScales));               // [kScales][128]
-  uint64_t* bars = (uint64_t*)(sslot + (S::kTma ? 0 : S::kScales * 128));
+  RowMask* smask = (RowMask*)(sslot + (S::kTma ? 0 : S::kScales * 128)); // [rows]
+  uint64_t* bars = (uint64_t*)(smask + (S::kTma ? 0 : S::kSoft));
   uint64_t* k_full = bars;
   uint64_t* k_empty = k_full + ST;
   uint64_t* v_full = k_empty + ST;
@@ -203,16 +262,17 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
   uint64_t* p_full = s_full + NQ;
   uint64_t* o_full = p_full + NQ;
   uint64_t* c_full = o_full + NQ;                  // the scales of a tile are there
-  uint32_t* tslot = (uint32_t*)(c_full + S::kScales);
+  uint64_t* i_full = c_full + S::kScales;          // an item is there
+  uint64_t* i_empty = i_full + S::kItems;
+  uint32_t* tslot = (uint32_t*)(i_empty + S::kItems);
   volatile int* abort_flag = (volatile int*)(tslot + 1);
-  Cursor* cursors = (Cursor*)(tslot + 4);          // [warps]
-  int64_t* sums = (int64_t*)(cursors + S::kThreads / 32);  // [batch + 1]
+  int64_t* sums = (int64_t*)(tslot + 4);           // [batch + 1]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  Cursor& c = cursors[warp];
   constexpr Cut cut = {S::kRows, 7};
   static_assert(kTcKeys == 1 << 7);
-  constexpr int kWarpMma = 4 * NQ, kWarpLoad = kWarpMma + S::kMma / 32;
+  constexpr int kWarpMma = 4 * NQ, kWarpPlan = kWarpMma + 1;
+  constexpr int kWarpLoad = S::kTma ? kWarpMma + 2 : (S::kSoft + S::kMma) / 32;
   pdl_launch_dependents();  // the join may be scheduled (it waits for this grid)
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
@@ -228,6 +288,10 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
       mbar_init(&o_full[q], 1);
     }
     for (int i = 0; i < S::kScales; ++i) mbar_init(&c_full[i], 128);
+    for (int i = 0; i < S::kItems; ++i) {
+      mbar_init(&i_full[i], 1);
+      mbar_init(&i_empty[i], 1 + S::kLoadWarps + 4 * NQ);
+    }
     *abort_flag = 0;
     a.redo[blockIdx.x] = 0;
     fence_barrier_init();
@@ -246,359 +310,401 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return mbar_wait(bar, parity, a.status, abort_flag);
   };
-  auto seek = [&] {
-    if (lane == 0) c.seek(a, sums, u0, cut);
-    __syncwarp();
-  };
-  auto step = [&] {  // a whole warp: the next unit
-    __syncwarp();
-    if (lane == 0 && ++c.u == c.t.units) c.next_tile(a, cut);
-    __syncwarp();
-  };
+  auto wait_item = [&](int n) { return wait(&i_full[n % S::kItems], (n / S::kItems) & 1); };
+  auto free_item = [&](int n) { mbar_arrive(&i_empty[n % S::kItems]); };
 
   // The deal stands in each role's own branch, where the compiler allots by it,
   // and every warp takes part in it, with work or without: a share is raised
   // once the others have been lowered.
   if (warp >= kWarpMma) {
-   if constexpr (S::kDeal && S::kTma)
-     deal_regs<S::kLaunchRegs, S::kLoadRegs>();
-   if (warp < kWarpLoad) {
-    // ------------------------------------------------------------ the MMAs
-    if constexpr (S::kDeal && !S::kTma)
-      deal_regs<S::kLaunchRegs, S::kMmaRegs>();
-    if (warp == kWarpMma && lane == 0 && left > 0) {
-      constexpr uint32_t is = idesc_bf16_f32(128, 128);
-      constexpr uint32_t io = idesc_bf16_f32(128, D) | (1u << 16);  // B is MN-major
-      c.seek(a, sums, u0, cut);
-      record_split(a, c, all, cta, shares);
-      int ns = 0, np = 0;                // key tiles whose S / O was issued
-      int nq_in[NQ] = {}, np_in[NQ] = {};  // phases of q_full and p_full
-      bool ok = true;
-      auto scores = [&](int q, bool first) {
-        if (first) {
-          ok = ok && wait(&q_full[q], nq_in[q] & 1);
-          ++nq_in[q];
-          tc_fence_after();
-        }
-        if (!ok) return;
-        const uint32_t qa = smem_u32(sq + q * S::kOperand),
-                       ka = smem_u32(sk + (ns % ST) * S::kOperand);
-#pragma unroll
-        for (int kc = 0; kc < KC; ++kc) {
-          const uint64_t da = smem_desc_k_sw128(qa + kc * S::kChunk);
-          const uint64_t db = smem_desc_k_sw128(ka + kc * S::kChunk);
-#pragma unroll
-          for (int s = 0; s < 4; ++s)
-            tc_mma_bf16(tmem + q * 128, da + 2 * s, db + 2 * s, is, (kc | s) != 0);
-        }
-        tc_commit(&s_full[q]);
-      };
-      int live_q = c.t.live > 128 ? 2 : 1;
-      bool first = true;
-      ok = wait(&k_full[0], 0);
-      tc_fence_after();
-      for (int q = 0; q < NQ && q < live_q; ++q) scores(q, true);
-      if (ok) tc_commit(&k_empty[0]);
-      ++ns;
-      while (ok) {
-        // the unit after this one
-        int live_next = live_q;
-        bool first_next = false;
-        if (left > 1 && ++c.u == c.t.units) {
+    if constexpr (S::kDeal && S::kTma) deal_regs<S::kLaunchRegs, S::kLoadRegs>();
+    if (warp < kWarpMma + S::kMma / 32 && !(S::kTma && warp == kWarpLoad)) {
+      if constexpr (S::kDeal && !S::kTma) deal_regs<S::kLaunchRegs, S::kMmaRegs>();
+      if (warp == kWarpPlan && lane == 0 && left > 0) {
+        // ------------------------------------------------------ the schedule
+        Cursor c;
+        c.seek(a, sums, u0, cut);
+        record_split(a, c, all, cta, shares);
+        for (int n = 0;; ++n) {
+          if (!wait(&i_empty[n % S::kItems], ((n / S::kItems) & 1) ^ 1)) break;
+          const int seg = min(left, c.t.units - c.u);
+          Item& it = items[n % S::kItems];
+          it = {c.b,   c.kvh, c.t.m0,    c.t.live,  c.rq.r0,   c.rq.n, c.rq.len, c.rq.p0,
+                c.u,   seg,   c.t.units, c.t.sinks, c.t.first, c.t.lo, c.t.hi,   c.t.sink};
+          mbar_arrive(&i_full[n % S::kItems]);
+          left -= seg;
+          if (left == 0) break;
           c.next_tile(a, cut);
-          live_next = c.t.live > 128 ? 2 : 1;
-          first_next = true;
         }
-        ok = ok && wait(&v_full[np % ST], (np / ST) & 1);
-        const uint64_t dv =
-            smem_desc_mn_sw128(smem_u32(sv + (np % ST) * S::kOperand), S::kChunk);
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          if (q < live_q) {
-            ok = ok && wait(&p_full[q], np_in[q] & 1);
-            ++np_in[q];
-            tc_fence_after();
-            if (!ok) break;
-#pragma unroll
-            for (int s = 0; s < 8; ++s)
-              tc_mma_ts(tmem + NQ * 128 + q * D, tmem + q * 128 + 8 * s, dv + 128 * s, io,
-                        !first || s != 0);
-            tc_commit(&o_full[q]);
-          }
-          if (left > 1 && q < live_next) {
-            if (q == 0) {
-              ok = ok && wait(&k_full[ns % ST], (ns / ST) & 1);
-              tc_fence_after();
-            }
-            scores(q, first_next);
-          }
-        }
-        if (!ok) break;
-        tc_commit(&v_empty[np % ST]);
-        ++np;
-        if (--left == 0) break;
-        tc_commit(&k_empty[ns % ST]);
-        ++ns;
-        live_q = live_next;
-        first = first_next;
-      }
-    }
-   } else {
-    // ------------------------------------------------------------ the loads
-    if constexpr (S::kDeal && !S::kTma)
-      deal_regs<S::kLaunchRegs, S::kLoadRegs>();
-    if (left > 0 && (!S::kTma || warp == kWarpLoad)) {
-    bool ok = true;
-    seek();
-    if constexpr (S::kTma) {
-      const int page = 1 << a.c.page_shift, box = min(page, 128);
-      for (int g = 0; left > 0 && ok; ++g, --left) {
-        const int base = unit_base(a, c.t, c.u, cut), st = g % ST;
-        const uint32_t parity = ((g / ST) & 1) ^ 1;
-        int y = 0;
-        const bool mine = base < 0 ? lane == 0 : lane * box < kTcKeys;
-        if (base >= 0 && mine) {
-          const int s = base + lane * box;
-          // a piece that no row sees, or on a page that is none: out of bounds, read as zeros
-          int64_t slot = -1;
-          if (piece_seen(c.t, s, box)) slot = a.c.slot(c.b, s, a.status);
-          y = (int)(slot < 0 ? ((int64_t)a.c.n_pages * a.c.Hkv) << a.c.page_shift
-                             : slot + ((int64_t)c.kvh << a.c.page_shift));
-        }
-        const uint32_t bytes = base < 0 ? (uint32_t)(a.Nmax + 1) * D * 2 : (uint32_t)S::kOperand;
-        auto load = [&](const CUtensorMap* cached, const CUtensorMap* tree, uint8_t* dst,
-                        uint64_t* full, uint64_t* empty) {
-          ok = ok && __all_sync(0xffffffffu, wait(empty, parity));
-          if (!ok) return;
-          if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-          __syncwarp();
-          if (!mine) return;
-#pragma unroll
-          for (int kc = 0; kc < KC; ++kc) {
-            if (base < 0)
-              tma_load_2d(dst + kc * S::kChunk, tree, full, c.kvh * D + kc * 64, c.rq.r0);
-            else
-              tma_load_2d(dst + kc * S::kChunk + lane * box * 128, cached, full, kc * 64, y);
-          }
+      } else if (warp == kWarpMma && lane == 0 && left > 0) {
+        // ---------------------------------------------------------- the MMAs
+        constexpr uint32_t is = idesc_bf16_f32(128, 128);
+        constexpr uint32_t io = idesc_bf16_f32(128, D) | (1u << 16);  // B is MN-major
+        int ns = 0, np = 0;                  // key tiles whose S / O was issued
+        uint32_t q_in = 0, p_in = 0;         // phases of q_full and p_full, a bit each
+        int ni = 0, in_item = 0, pairs = 0;  // items taken; units left of one, its row tiles
+        bool ok = true;
+        auto take = [&] {
+          ok = ok && wait_item(ni);
+          pairs = items[ni % S::kItems].live > 128 ? 2 : 1;
+          in_item = items[ni % S::kItems].seg;
+          free_item(ni++);
         };
-        load(&maps.k, &maps.kt, sk + st * S::kOperand, &k_full[st], &k_empty[st]);
-        __syncwarp();
-        load(&maps.v, &maps.vt, sv + st * S::kOperand, &v_full[st], &v_empty[st]);
-        if (left > 1) step();
+        auto scores = [&](int q, bool first) {
+          if (first) {
+            ok = ok && wait(&q_full[q], (q_in >> q) & 1);
+            q_in ^= 1u << q;
+            tc_fence_after();
+          }
+          if (!ok) return;
+          const uint32_t qa = desc_lo_k(smem_u32(sq) + q * S::kOperand);
+          const uint32_t ka = desc_lo_k(smem_u32(sk) + ns % ST * S::kOperand);
+#pragma unroll
+          for (int s = 0; s < 4 * KC; ++s) {
+            const uint32_t step = (s >> 2) * (S::kChunk >> 4) + (s & 3) * 2;
+            mma_ss(tmem + q * 128, qa + step, ka + step, is, s != 0);
+          }
+          tc_commit(&s_full[q]);
+        };
+        take();
+        int live_q = 0, live_next = pairs;
+        bool first = true, first_next = true;
+        // turn t: O of unit t - 1, S of unit t
+        for (int more = left; ok; --more) {
+          const bool pv = live_q > 0, sc = more > 0;
+          if (pv) ok = wait(&v_full[np % ST], (np / ST) & 1);
+          const uint32_t va = desc_lo_mn(smem_u32(sv) + np % ST * S::kOperand, S::kChunk);
+#pragma unroll 1
+          for (int q = 0; q < NQ; ++q) {
+            if (q < live_q) {
+              ok = ok && wait(&p_full[q], (p_in >> q) & 1);
+              p_in ^= 1u << q;
+              tc_fence_after();
+              if (!ok) break;
+#pragma unroll
+              for (int s = 0; s < 8; ++s)
+                mma_ts(tmem + NQ * 128 + q * D, tmem + q * 128 + 8 * s, va + 128 * s, io,
+                       !first || s != 0);
+              // (between tiles s_full of the next one says it: it tracks all products so far)
+              if (!sc || first_next) tc_commit(&o_full[q]);
+            }
+            if (sc && q < live_next) {
+              if (q == 0) {
+                ok = ok && wait(&k_full[ns % ST], (ns / ST) & 1);
+                tc_fence_after();
+              }
+              scores(q, first_next);
+            }
+          }
+          if (!ok) break;
+          if (pv) {
+            tc_commit(&v_empty[np % ST]);
+            ++np;
+          }
+          if (!sc) break;
+          tc_commit(&k_empty[ns % ST]);
+          ++ns;
+          live_q = live_next;
+          first = first_next;
+          first_next = --in_item == 0;
+          if (first_next && more > 1) {
+            take();
+            live_next = pairs;
+          }
+        }
       }
     } else {
-      // 8-bit codes: a thread takes every 128th 16-byte piece of the tile.  The
-      // slots of a tile's positions (one a thread) are looked up two tiles ahead,
-      // its codes are in registers one tile ahead.
-      constexpr int kRowPieces = D / 16, kPieces = 128 * kRowPieces / 128;
-      const int lt = tid - kWarpLoad * 32;
-      const int piece = lt % kRowPieces, row0 = lt / kRowPieces;
-      uint4 kw[kPieces], vw[kPieces];
-      float kscale = 0.f, vscale = 0.f;
-      // this thread's slot of the tile at the cursor, -1: read as zeros
-      auto look_up = [&]() -> int {
-        const int s = unit_base(a, c.t, c.u, cut) + lt;
-        if (s < lt || !piece_seen(c.t, s, 1)) return -1;
-        const int64_t slot = a.c.slot(c.b, s, a.status);
-        return slot < 0 ? -1 : (int)(slot + ((int64_t)c.kvh << a.c.page_shift));
-      };
-      auto plan = [&](int g, int slot) {
-        sslot[(g % S::kScales) * 128 + lt] = slot;
-        if (lt == 0)
-          sinfo[g % S::kScales] = make_int4(unit_base(a, c.t, c.u, cut), c.kvh, c.rq.r0, c.rq.n);
-      };
-      auto sync = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
-      auto fetch = [&](int g, const void* cache, const float* scales, uint4 (&w)[kPieces],
-                       float& scale) {
-        if (sinfo[g % S::kScales].x < 0) return;
-        const int* slots = sslot + (g % S::kScales) * 128;
+      // -------------------------------------------------------------- the loads
+      if constexpr (S::kDeal && !S::kTma) deal_regs<S::kLaunchRegs, S::kLoadRegs>();
+      bool ok = true;
+      if constexpr (S::kTma) {
+        const int page = 1 << a.c.page_shift, box = min(page, 128);
+        int g = 0;
+        for (int n = 0; left > 0 && ok; ++n) {
+          ok = __all_sync(0xffffffffu, wait_item(n));
+          if (!ok) break;
+          const Item it = items[n % S::kItems];
+          __syncwarp();
+          if (lane == 0) free_item(n);
+          left -= it.seg;
+          for (int u = it.u; u < it.u + it.seg && ok; ++u, ++g) {
+            const int base = it.base(a, u), st = g % ST;
+            const uint32_t parity = ((g / ST) & 1) ^ 1;
+            int y = 0;
+            const bool mine = base < 0 ? lane == 0 : lane * box < kTcKeys;
+            if (base >= 0 && mine) {
+              const int s = base + lane * box;
+              // a piece that no row sees, or on a page that is none: out of bounds, read as zeros
+              int64_t slot = -1;
+              if (it.seen(s, box)) slot = a.c.slot(it.b, s, a.status);
+              y = (int)(slot < 0 ? ((int64_t)a.c.n_pages * a.c.Hkv) << a.c.page_shift
+                                 : slot + ((int64_t)it.kvh << a.c.page_shift));
+            }
+            const uint32_t bytes =
+                base < 0 ? (uint32_t)(a.Nmax + 1) * D * 2 : (uint32_t)S::kOperand;
+            auto load = [&](const CUtensorMap* cached, const CUtensorMap* tree, uint8_t* dst,
+                            uint64_t* full, uint64_t* empty) {
+              ok = __all_sync(0xffffffffu, ok && wait(empty, parity));
+              if (!ok) return;
+              if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+              __syncwarp();
+              if (mine) {
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          const int slot = slots[row0 + i * (128 / kRowPieces)];
-          w[i] = make_uint4(0, 0, 0, 0);
-          if (slot >= 0)
-            w[i] = __ldg((const uint4*)((const uint8_t*)cache + (int64_t)slot * D + piece * 16));
-        }
-        const int slot = slots[lt];
-        scale = slot < 0 ? 0.f : __ldg(scales + slot);
-      };
-      // the tile into shared memory as bf16: codes that are in registers, or the tree's rows
-      auto place = [&](int g, uint8_t* dst, const void* tree, const uint4 (&w)[kPieces]) {
-        const int4 info = sinfo[g % S::kScales];
-        if (info.x < 0) {
-          const uint16_t* rows = (const uint16_t*)tree;
-          for (int x = lt; x < 128 * KC * 8; x += 128) {
-            const int cc = x % (KC * 8), r = x / (KC * 8);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (r < info.w)
-              v = *(const uint4*)(rows + (((int64_t)info.z + r) * a.c.Hkv + info.y) * D + cc * 8);
-            *(uint4*)(dst + (cc >> 3) * S::kChunk + sw128(r, cc & 7)) = v;
+                for (int kc = 0; kc < KC; ++kc) {
+                  if (base < 0)
+                    tma_load_2d(dst + kc * S::kChunk, tree, full, it.kvh * D + kc * 64, it.r0);
+                  else
+                    tma_load_2d(dst + kc * S::kChunk + lane * box * 128, cached, full, kc * 64, y);
+                }
+              }
+              __syncwarp();
+            };
+            load(&maps.k, &maps.kt, sk + st * S::kOperand, &k_full[st], &k_empty[st]);
+            load(&maps.v, &maps.vt, sv + st * S::kOperand, &v_full[st], &v_empty[st]);
           }
-          return;
         }
-        uint8_t* at = dst + (piece >> 2) * S::kChunk;
-        // the lanes of the second 64 columns store their halves in the other order: all 32 banks
-        const int c0 = (piece & 3) * 2, odd = piece >> 2;
+      } else if (left > 0) {
+        // 8-bit codes: a thread takes every 128th 16-byte piece of the tile.  The
+        // slots of a tile's positions (one a thread) are looked up two tiles ahead,
+        // its codes are in registers one tile ahead.
+        constexpr int kRowPieces = D / 16, kPieces = 128 * kRowPieces / 128;
+        constexpr int kNone = INT_MIN;
+        const int lt = tid - kWarpLoad * 32;
+        const int piece = lt % kRowPieces, row0 = lt / kRowPieces;
+        uint4 kw[kPieces], vw[kPieces];
+        float kscale = 0.f, vscale = 0.f;
+        int n = 0, u = 0;  // item and unit that look_up is at
+        auto sync = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+        // page of this thread's position of the unit; kNone: not seen
+        auto look_up = [&]() -> int {
+          const Item& it = items[n % S::kItems];
+          const int s = it.base(a, u) + lt;
+          if (s < lt || !it.seen(s, 1)) return kNone;
+          const int pi = s >> a.c.page_shift;
+          return pi < a.c.max_pages ? __ldg(a.c.table + (int64_t)it.b * a.c.max_pages + pi) : -1;
+        };
+        // writes down its slot (-1: read as zeros), and goes on to the next unit
+        auto plan = [&](int g, int page, bool more) {
+          const Item& it = items[n % S::kItems];
+          const int base = it.base(a, u), at = (base + lt) & ((1 << a.c.page_shift) - 1);
+          int slot = -1;
+          if (page >= 0 && page < a.c.n_pages)
+            slot = ((page * a.c.Hkv + it.kvh) << a.c.page_shift) + at;
+          else if (page != kNone)
+            set_status(a.status, DT_EDEVICE);
+          sslot[(g % S::kScales) * 128 + lt] = slot;
+          if (lt == 0) sinfo[g % S::kScales] = make_int4(base, it.kvh, it.r0, it.n);
+          if (more && ++u == it.u + it.seg) {
+            __syncwarp();
+            if (lane == 0) free_item(n);
+            ++n;
+            ok = __all_sync(0xffffffffu, ok && wait_item(n));
+            u = items[n % S::kItems].u;
+          }
+        };
+        auto fetch = [&](int g, const void* cache, const float* scales, uint4 (&w)[kPieces],
+                         float& scale) {
+          if (sinfo[g % S::kScales].x < 0) return;
+          const int* slots = sslot + (g % S::kScales) * 128;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          const int r = row0 + i * (128 / kRowPieces);
-          uint32_t o[8];
-          const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+          for (int i = 0; i < kPieces; ++i) {
+            const int slot = slots[row0 + i * (128 / kRowPieces)];
+            w[i] = make_uint4(0, 0, 0, 0);
+            if (slot >= 0)
+              w[i] = __ldg((const uint4*)((const uint8_t*)cache + (int64_t)slot * D + piece * 16));
+          }
+          const int slot = slots[lt];
+          scale = slot < 0 ? 0.f : __ldg(scales + slot);
+        };
+        // the tile into shared memory as bf16: codes that are in registers, or the tree's rows
+        auto place = [&](int g, uint8_t* dst, const void* tree, const uint4 (&w)[kPieces]) {
+          const int4 info = sinfo[g % S::kScales];
+          if (info.x < 0) {
+            const uint16_t* rows = (const uint16_t*)tree;
+#pragma unroll 2
+            for (int x = lt; x < 128 * KC * 8; x += 128) {
+              const int cc = x % (KC * 8), r = x / (KC * 8);
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (r < info.w)
+                v = *(const uint4*)(rows + (((int64_t)info.z + r) * a.c.Hkv + info.y) * D + cc * 8);
+              *(uint4*)(dst + (cc >> 3) * S::kChunk + sw128(r, cc & 7)) = v;
+            }
+            return;
+          }
+          // the lanes of the second 64 columns store their halves in the other order: all 32 banks
+          // (rows of a thread are 128 / kRowPieces apart, a multiple of 8: one swizzle for all)
+          const int c0 = (piece & 3) * 2, odd = piece >> 2;
+          uint8_t* at = dst + (piece >> 2) * S::kChunk;
+          uint8_t* at0 = at + sw128(row0, c0 + odd);
+          uint8_t* at1 = at + sw128(row0, c0 + 1 - odd);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) codes_to_bf16<CT>(in[e], o[2 * e], o[2 * e + 1]);
-          *(uint4*)(at + sw128(r, c0 + odd)) =
-              odd ? make_uint4(o[4], o[5], o[6], o[7]) : make_uint4(o[0], o[1], o[2], o[3]);
-          *(uint4*)(at + sw128(r, c0 + 1 - odd)) =
-              odd ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(o[4], o[5], o[6], o[7]);
-        }
-      };
-      plan(0, look_up());
-      if (left > 1) {
-        step();
-        plan(1, look_up());
-      }
-      sync();
-      fetch(0, a.c.k, a.c.ks, kw, kscale);
-      fetch(0, a.c.v, a.c.vs, vw, vscale);
-      for (int g = 0; left > 0; ++g, --left) {
-        const int st = g % ST;
-        const uint32_t parity = ((g / ST) & 1) ^ 1;
-        int ahead = -1;
-        if (left > 2) {
-          step();
-          ahead = look_up();
-        }
-        // The scales' slot was last used by tile g - 4.  k_empty means that S of
-        // tile g - ST is complete, which was issued only after the softmax of
-        // the tile before it had handed over P; so tile g - ST - 1 >= g - 4 is done.
-        float* scales = sscale + (g % S::kScales) * 256;
-        // (a warp that gives up goes on to the barriers, so that the others pass them)
-        ok = __all_sync(0xffffffffu, ok && wait(&k_empty[st], parity));
-        if (ok) {
-          place(g, sk + st * S::kOperand, a.kt, kw);
-          const bool tree = sinfo[g % S::kScales].x < 0;
-          scales[lt] = tree ? 1.f : kscale;
-          scales[128 + lt] = tree ? 1.f : vscale;
-          fence_async_smem();
-          mbar_arrive(&k_full[st]);
-          mbar_arrive(&c_full[g % S::kScales]);
-          // the next tile's loads are on their way while this one is worked on
-          if (left > 1) fetch(g + 1, a.c.k, a.c.ks, kw, kscale);
-          ok = __all_sync(0xffffffffu, wait(&v_empty[st], parity));
-        }
-        if (ok) {
-          place(g, sv + st * S::kOperand, a.vt, vw);
-          fence_async_smem();
-          mbar_arrive(&v_full[st]);
-          if (left > 1) fetch(g + 1, a.c.v, a.c.vs, vw, vscale);
-        }
-        if (left > 2) plan(g + 2, ahead);
+          for (int i = 0; i < kPieces; ++i) {
+            uint32_t o[8];
+            const uint32_t in[4] = {odd ? w[i].z : w[i].x, odd ? w[i].w : w[i].y,
+                                    odd ? w[i].x : w[i].z, odd ? w[i].y : w[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) codes_to_bf16<CT>(in[e], o[2 * e], o[2 * e + 1]);
+            *(uint4*)(at0 + i * (128 / kRowPieces) * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+            *(uint4*)(at1 + i * (128 / kRowPieces) * 128) = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+        };
+        ok = __all_sync(0xffffffffu, wait_item(0));
+        u = items[0].u;
+        if (ok) plan(0, look_up(), left > 1);
+        if (ok && left > 1) plan(1, look_up(), left > 2);
         sync();
+        if (ok) {
+          fetch(0, a.c.k, a.c.ks, kw, kscale);
+          fetch(0, a.c.v, a.c.vs, vw, vscale);
+        }
+        for (int g = 0; left > 0; ++g, --left) {
+          const int st = g % ST;
+          const uint32_t parity = ((g / ST) & 1) ^ 1;
+          // (a warp that gives up goes on to the barriers, so that the others pass them)
+          int ahead = kNone;
+          if (ok && left > 2) ahead = look_up();
+          // The scales' slot was last used by tile g - 4.  k_empty means that S of
+          // tile g - ST is complete, which was issued only after the softmax of
+          // the tile before it had handed over P; so tile g - ST - 1 >= g - 4 is done.
+          float* scales = sscale + (g % S::kScales) * 256;
+          ok = __all_sync(0xffffffffu, ok && wait(&k_empty[st], parity));
+          if (ok) {
+            place(g, sk + st * S::kOperand, a.kt, kw);
+            const bool tree = sinfo[g % S::kScales].x < 0;
+            scales[lt] = tree ? 1.f : kscale;
+            scales[128 + lt] = tree ? 1.f : vscale;
+            fence_async_smem();
+            mbar_arrive(&k_full[st]);
+            mbar_arrive(&c_full[g % S::kScales]);
+            // the next tile's loads are on their way while this one is worked on
+            if (left > 1) fetch(g + 1, a.c.k, a.c.ks, kw, kscale);
+            ok = __all_sync(0xffffffffu, wait(&v_empty[st], parity));
+          }
+          if (ok) {
+            place(g, sv + st * S::kOperand, a.vt, vw);
+            fence_async_smem();
+            mbar_arrive(&v_full[st]);
+            if (left > 1) fetch(g + 1, a.c.v, a.c.vs, vw, vscale);
+            if (left > 2) plan(g + 2, ahead, left > 3);
+          }
+          sync();
+        }
       }
     }
-   }
-   }
   } else {
-    // ---------------------------------------------------------- the softmax
+    // ------------------------------------------------------------ the softmax
     if constexpr (S::kDeal) deal_regs<S::kLaunchRegs, S::kSoftRegs>();
-   if (left > 0) {
     const int q = warp >> 2, row = tid & 127;
     const uint32_t quad = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + quad + q * 128, to = tmem + quad + NQ * 128 + q * D;
     uint8_t* my_q = sq + q * S::kOperand;
     const float sl2 = a.scale * kL2e;
-    seek();
-    auto next_tile = [&] {
-      __syncwarp();
-      if (lane == 0) c.next_tile(a, cut);
-      __syncwarp();
-    };
-    // the row tile's queries into shared memory, zeros where there is no row
-    auto load_q = [&] {
-      const int m0 = c.t.m0 + q * 128, live = c.t.live - q * 128, r0 = c.rq.r0, h0 = c.kvh * a.G;
+    // item n's queries into shared memory, zeros where there is no row
+    auto start_q = [&](int n) {
+      const Item& it = items[n % S::kItems];
+      const int m0 = it.m0 + q * 128, live = it.live - q * 128, r0 = it.r0, h0 = it.kvh * a.G;
 #pragma unroll 4
       for (int x = row; x < 128 * KC * 8; x += 128) {
-        const int cc = x % (KC * 8), r = x / (KC * 8);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < live) {
-          const int m = m0 + r;
-          v = *(const uint4*)((const uint16_t*)a.q + (r0 + (int64_t)(m / a.G)) * a.ld_q +
-                              ((int64_t)h0 + m % a.G) * D + cc * 8);
-        }
-        *(uint4*)(my_q + (cc >> 3) * S::kChunk + sw128(r, cc & 7)) = v;
+        const int cc = x % (KC * 8), r = x / (KC * 8), m = m0 + (r < live ? r : 0);
+        cp16(smem_u32(my_q + (cc >> 3) * S::kChunk + sw128(r, cc & 7)),
+             (const uint16_t*)a.q + (r0 + (int64_t)(m / a.G)) * a.ld_q +
+                 ((int64_t)h0 + m % a.G) * D + cc * 8,
+             r < live);
       }
+    };
+    auto finish_q = [&] {
+      asm volatile("cp.async.wait_all;" ::: "memory");
       fence_async_smem();
       mbar_arrive(&q_full[q]);
     };
-    if (q * 128 < c.t.live) load_q();
-    bool ok = true;
-    int n_done = 0;  // key tiles of this row tile's barriers
-    int g = 0;       // key tiles of the CTA
-    bool head = c.u > 0;
-    while (left > 0) {
-      const int seg = min(left, c.t.units - c.u);
-      if (q * 128 >= c.t.live) {  // no row of this item is in the second row tile
+    bool ok = true, q_started = false;
+    int n_done = 0, n_item = 0;  // key tiles and row tiles of this warpgroup's barriers
+    int g = 0;                   // key tiles of the CTA
+    for (int n = 0; left > 0; ++n) {
+      ok = __all_sync(0xffffffffu, wait_item(n));
+      if (!ok) break;
+      const Item& it = items[n % S::kItems];
+      const int seg = it.seg, live = it.live - q * 128;
+      left -= seg;
+      if (live <= 0) {  // no row of this item is in the second row tile
         g += seg;
-        left -= seg;
-        head = false;
-        if (left > 0) {
-          next_tile();
-          if (q * 128 < c.t.live) load_q();
-        }
+        __syncwarp();
+        if (lane == 0) free_item(n);
         continue;
       }
-      const bool there = q * 128 + row < c.t.live;
-      const int m_at = c.t.m0 + q * 128 + (there ? row : 0);
-      const int i = m_at / a.G, h = c.kvh * a.G + m_at % a.G;
-      RowMask mask;
-      mask.vis = visible(a, row_position(a, c.rq, c.b, i), c.rq.len);
-      mask.tree = 0;
-      mask.top = 0;
-      if (a.kt) {
-        const uint64_t anc = i ? a.anc[(int64_t)c.b * a.Nmax + i - 1] : 0ull;
-        mask.tree = 1ull | (anc << 1);
-        mask.top = (uint32_t)(anc >> 63);
-        if (c.rq.n < 64) mask.tree &= (1ull << c.rq.n) - 1;
-        if (c.rq.n < 65) mask.top = 0;
+      if (!q_started) {
+        start_q(n);
+        finish_q();
       }
-      // key tiles in [whole_lo, whole_hi) need no mask for any row of the tile
-      int whole_lo = mask.vis.first, whole_hi = mask.vis.last;
-      whole_lo = __reduce_max_sync(0xffffffffu, whole_lo);
-      whole_hi = __reduce_min_sync(0xffffffffu, whole_hi);
-      float m = -INFINITY, l = 0.f;
+      q_started = false;
+      const bool head = it.u > 0, whole = it.u == 0 && seg == it.units;
+      const bool there = row < live;
+      const int m_at = it.m0 + q * 128 + (there ? row : 0);
+      const int i = m_at / a.G, h = it.kvh * a.G + m_at % a.G;
+      const PagedRequest rq = {it.r0, it.n, it.len, it.p0};
+      RowMask mask;
+      mask.vis = visible(a, row_position(a, rq, it.b, i), rq.len);
+      mask.tree[0] = mask.tree[1] = mask.tree[2] = 0;
+      if (a.kt) {
+        const uint64_t anc = i ? a.anc[(int64_t)it.b * a.Nmax + i - 1] : 0ull;
+        mask.tree[0] = (1u | ((uint32_t)anc << 1)) & low_bits(rq.n);
+        mask.tree[1] = (uint32_t)(anc >> 31) & low_bits(rq.n - 32);
+        mask.tree[2] = (uint32_t)(anc >> 63) & low_bits(rq.n - 64);
+      }
+      const bool sees = a.kt || mask.vis.sink > 0 || mask.vis.last > mask.vis.first;
+      if constexpr (!S::kTma) {
+        smask[q * 128 + row] = mask;
+        __syncwarp();
+      }
+      // key tiles in [whole_lo, whole_hi) need no mask for any row of the warp
+      const int whole_lo = __reduce_max_sync(0xffffffffu, mask.vis.first);
+      const int whole_hi = __reduce_min_sync(0xffffffffu, mask.vis.last);
+      float m = -INFINITY, l = 0.f;  // (bf16 cache) this thread's row
+      // (8-bit cache) rows lane / 4 + 8 x of the warp; each sum is that of this lane's columns
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, l4[4] = {0.f, 0.f, 0.f, 0.f};
+      // O times a factor per row: the products so far are complete (s_full)
+      auto rescale = [&](float keep) {
+#pragma unroll 1
+        for (int w = 0; w < D / 16; ++w) {
+          uint32_t x[16];
+          tmem_ld16_nowait(to + 16 * w, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * keep);
+          tmem_st16(to + 16 * w, x);
+        }
+      };
       for (int k = 0; k < seg; ++k, ++g, ++n_done) {
-        const int base = unit_base(a, c.t, c.u + k, cut);
+        const int base = it.base(a, it.u + k);
         const bool masked = base < whole_lo || base + kTcKeys > whole_hi;
-        const float* scales = sscale + (g % S::kScales) * 256;
-        ok = ok && wait(&s_full[q], n_done & 1);
+        ok = wait(&s_full[q], n_done & 1);
         if constexpr (!S::kTma)
           ok = ok && wait(&c_full[g % S::kScales], (g / S::kScales) & 1);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         tc_fence_after();
-        auto tile = [&](auto masked_c) -> bool {
-          constexpr bool kMasked = decltype(masked_c)::value;
+        if (k == seg - 1 && left > 0) {
+          // S is complete, so Q's place is free: the next row tile's is on its way
+          ok = __all_sync(0xffffffffu, wait_item(n + 1));
+          if (!ok) break;
+          q_started = items[(n + 1) % S::kItems].live > q * 128;
+          if (q_started) start_q(n + 1);
+        }
+        if constexpr (S::kTma) {
           constexpr int kKeep = S::kKeep;
           // ---- the row's largest score of this tile
           uint32_t r[kKeep][32];
-          auto load = [&](int w) { tmem_ld32(ts + 32 * w, r[w % kKeep]); };
-          // scores of part w: times the keys' scales, -infinity where the row does not see
-          auto finish = [&](int w) {
-            const uint32_t see = kMasked ? mask.word(base, w) : 0;
+          auto load = [&](int w0) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              uint32_t* x = r[w % kKeep] + e;
-              if constexpr (!S::kTma) {
-                const float4 f = *(const float4*)(scales + 32 * w + e);
-                mul2(x[0], x[1], f.x, f.y);
-                mul2(x[2], x[3], f.z, f.w);
-              }
-              if constexpr (kMasked) {
+            for (int w = w0; w < w0 + kKeep; ++w) tmem_ld32(ts + 32 * w, r[w - w0]);
+            tmem_wait_ld();
+            if (masked) {
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
-                  x[y] = (see >> (e + y)) & 1u ? x[y] : 0xff800000u;
+              for (int w = w0; w < w0 + kKeep; ++w) {
+                const uint32_t see = mask.word(base, w);
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  r[w - w0][e] = (see >> e) & 1u ? r[w - w0][e] : 0xff800000u;
               }
             }
           };
@@ -606,17 +712,13 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
           // the first parts are read twice where not all of them fit the registers
 #pragma unroll
           for (int w0 = 4 - kKeep; w0 >= 0; w0 -= kKeep) {
+            load(w0);
 #pragma unroll
-            for (int w = w0; w < w0 + kKeep; ++w) load(w);
-            tmem_wait_ld();
-#pragma unroll
-            for (int w = w0; w < w0 + kKeep; ++w) {
-              finish(w);
+            for (int w = 0; w < kKeep; ++w)
 #pragma unroll
               for (int e = 0; e < 32; e += 2)
-                t4[(e / 2) % 4] = fmaxf(fmaxf(t4[(e / 2) % 4], __uint_as_float(r[w % kKeep][e])),
-                                        __uint_as_float(r[w % kKeep][e + 1]));
-            }
+                t4[(e / 2) % 4] = fmaxf(fmaxf(t4[(e / 2) % 4], __uint_as_float(r[w][e])),
+                                        __uint_as_float(r[w][e + 1]));
           }
           const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * sl2;
           // ---- the maximum in use
@@ -627,30 +729,14 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
             const float keep = m == now ? 1.f : ex2(m - now);
             l *= keep;
             m = now;
-            if (!__all_sync(0xffffffffu, wait(&o_full[q], (n_done - 1) & 1))) return false;
-            tc_fence_after();
-            uint32_t x[16];
-#pragma unroll
-            for (int w = 0; w < D / 16; ++w) {
-              tmem_ld16_nowait(to + 16 * w, x);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * keep);
-              tmem_st16(to + 16 * w, x);
-            }
+            rescale(keep);
           }
           const float less = m == -INFINITY ? 0.f : -m;
           // ---- weights, in bf16 for the second product, over the scores
           float la[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            if (w >= kKeep && w % kKeep == 0) {
-#pragma unroll
-              for (int x = w; x < w + kKeep; ++x) load(x);
-              tmem_wait_ld();
-#pragma unroll
-              for (int x = w; x < w + kKeep; ++x) finish(x);
-            }
+            if (w > 0 && w % kKeep == 0) load(w);
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
@@ -662,39 +748,19 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
               for (int y = 0; y < 4; ++y) p[y] = ex2(p[y]);
               add2(la[0], la[1], p[0], p[1]);
               add2(la[2], la[3], p[2], p[3]);
-              if constexpr (!S::kTma) {
-                const float4 f = *(const float4*)(scales + 128 + 32 * w + e);
-                uint32_t z[4];
-#pragma unroll
-                for (int y = 0; y < 4; ++y) z[y] = __float_as_uint(p[y]);
-                mul2(z[0], z[1], f.x, f.y);
-                mul2(z[2], z[3], f.z, f.w);
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                  // (a scale of a place that the row does not see may be NaN)
-                  p[y] = kMasked && x[y] == 0xff800000u ? 0.f : __uint_as_float(z[y]);
-                }
-              }
               pk[e / 2] = pack2(p[0], p[1]);
               pk[e / 2 + 1] = pack2(p[2], p[3]);
             }
             tmem_st16(ts + 16 * w, pk);
           }
           l += (la[0] + la[1]) + (la[2] + la[3]);
-          return true;
-        };
-        ok = masked ? tile(std::true_type()) : tile(std::false_type());
-        if (!ok) break;
-        if constexpr (S::kTma) {
           // V rows that are no positions of the request may hold anything: zeros, before 0 * NaN
-          const int valid = base < 0 ? c.rq.n : c.rq.len - base;
+          const int valid = base < 0 ? rq.n : rq.len - base;
           if (valid < kTcKeys) {
-            ok = wait(&v_full[g % ST], (g / ST) & 1);
-            if (!__all_sync(0xffffffffu, ok)) {
-              ok = false;
-              break;
-            }
+            ok = __all_sync(0xffffffffu, wait(&v_full[g % ST], (g / ST) & 1));
+            if (!ok) break;
             uint8_t* v = sv + (g % ST) * S::kOperand;
+#pragma unroll 1
             for (int x = row; x < 128 * KC * 8; x += 128) {
               const int r8 = x / (KC * 8), cc = x % (KC * 8);
               if (r8 >= valid)
@@ -702,30 +768,136 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
             }
             fence_async_smem();
           }
+        } else {
+          // The keys' scales multiply columns, and a thread of a whole row would
+          // read each of them: 3 x 128 shared loads a tile that all lanes repeat.
+          // In fragment layout a lane has a quarter of the columns of four rows.
+          // (A scale of NaN at a place that a row does not see makes its sum NaN,
+          // with a finite weight sum: such rows are done again, see paged_row.)
+          const float* kscale = sscale + (g % S::kScales) * 256 + 2 * (lane & 3);
+          const RowMask* rows = smask + q * 128 + 32 * (warp & 3) + (lane >> 2);
+          uint32_t r[2][32];  // 64 columns of rows lane / 4 + 0, 8 and + 16, 24
+          // scores of half hh: times the keys' scales, -infinity where the row does not see
+          auto load = [&](int hh) {
+            tmem_ld_frag(ts + 64 * hh, r[0]);
+            tmem_ld_frag(ts + (16u << 16) + 64 * hh, r[1]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float2 f = *(const float2*)(kscale + 64 * hh + 8 * j);
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                mul2(r[x >> 1][4 * j + 2 * (x & 1)], r[x >> 1][4 * j + 2 * (x & 1) + 1], f.x, f.y);
+            }
+            if (masked) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  const uint32_t see = rows[8 * x].word(base, 2 * hh + y) >> (2 * (lane & 3));
+#pragma unroll
+                  for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                      uint32_t& z = r[x >> 1][4 * (4 * y + j) + 2 * (x & 1) + e];
+                      z = (see >> (8 * j + e)) & 1u ? z : 0xff800000u;
+                    }
+                }
+            }
+          };
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int hh = 1; hh >= 0; --hh) {
+            load(hh);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                top[x] = fmaxf(fmaxf(top[x], __uint_as_float(r[x >> 1][4 * j + 2 * (x & 1)])),
+                               __uint_as_float(r[x >> 1][4 * j + 2 * (x & 1) + 1]));
+          }
+          bool grows = false;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
+            top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2)) * sl2;
+            grows |= top[x] > m4[x] + kRescale;
+          }
+          if (k == 0) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) m4[x] = top[x];
+          } else if (__any_sync(0xffffffffu, grows)) {
+            float mine4 = 1.f;  // the factor of this thread's row in TMEM
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float now = fmaxf(m4[x], top[x]);
+              const float keep = m4[x] == now ? 1.f : ex2(m4[x] - now);
+              l4[x] *= keep;
+              m4[x] = now;
+              const float v = __shfl_sync(0xffffffffu, keep, 4 * (lane & 7));
+              if (lane >> 3 == x) mine4 = v;
+            }
+            rescale(mine4);
+          }
+          float less[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) less[x] = m4[x] == -INFINITY ? 0.f : -m4[x];
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            if (hh) load(hh);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const float2 f = *(const float2*)(kscale + 128 + 64 * hh + 8 * j);
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  const int x = 2 * t + z;
+                  float p0, p1;
+                  fma2(r[t][4 * j + 2 * z], r[t][4 * j + 2 * z + 1], sl2, less[x], p0, p1);
+                  p0 = ex2(p0);
+                  p1 = ex2(p1);
+                  l4[x] += p0 + p1;
+                  uint32_t w0 = __float_as_uint(p0), w1 = __float_as_uint(p1);
+                  mul2(w0, w1, f.x, f.y);
+                  pk[2 * j + z] = pack2(__uint_as_float(w0), __uint_as_float(w1));
+                }
+              }
+              tmem_st_frag16(ts + (t ? 16u << 16 : 0u) + 32 * hh, pk);
+            }
+          }
         }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&p_full[q]);
       }
       if (!ok) break;
-      left -= seg;
-      const bool whole = c.u == 0 && seg == c.t.units;
-      const int r0 = c.rq.r0;
-      if (left > 0) {
-        next_tile();
-        if (q * 128 < c.t.live) load_q();
+      if (q_started) finish_q();
+      __syncwarp();
+      if (lane == 0) free_item(n);  // (what is left of it is in registers)
+      if constexpr (!S::kTma) {
+        // statistics of this thread's row
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          l4[x] += __shfl_xor_sync(0xffffffffu, l4[x], 1);
+          l4[x] += __shfl_xor_sync(0xffffffffu, l4[x], 2);
+          const float mv = __shfl_sync(0xffffffffu, m4[x], 4 * (lane & 7));
+          const float lv = __shfl_sync(0xffffffffu, l4[x], 4 * (lane & 7));
+          if (lane >> 3 == x) m = mv, l = lv;
+        }
       }
-      ok = __all_sync(0xffffffffu, wait(&o_full[q], (n_done - 1) & 1));
+      ok = __all_sync(0xffffffffu, wait(&o_full[q], n_item & 1));
       if (!ok) break;
+      ++n_item;
       tc_fence_after();
       if (whole) {
-        const bool sees = a.kt || mask.vis.sink > 0 || mask.vis.last > mask.vis.first;
         const float inv = row_factor(l, sees);
-        uint16_t* out = (uint16_t*)a.out + (((int64_t)r0 + i) * a.Hq + h) * D;
+        uint16_t* out = (uint16_t*)a.out + (((int64_t)rq.r0 + i) * a.Hq + h) * D;
         float odd = 0.f;  // NaN once an output is infinite or NaN
-        uint32_t r[32];
-#pragma unroll
+#pragma unroll 1
         for (int w = 0; w < D / 32; ++w) {
+          uint32_t r[32];
           tmem_ld32(to + 32 * w, r);
           tmem_wait_ld();
           uint4 pk[4];
@@ -746,10 +918,10 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
       } else {
         const int64_t at = (int64_t)(2 * cta + (head ? 0 : 1)) * a.part_rows + q * 128 + row;
         float* po = a.part_o + at * D;
-        uint32_t r[32];
         if (there) a.part_ml[at] = make_float2(m, l);
-#pragma unroll
+#pragma unroll 1
         for (int w = 0; w < D / 32; ++w) {
+          uint32_t r[32];
           tmem_ld32(to + 32 * w, r);
           tmem_wait_ld();
           if (there) {
@@ -760,9 +932,7 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
         }
       }
       tc_fence_before();
-      head = false;
     }
-   }
   }
   __syncwarp();
   if (*abort_flag) {
