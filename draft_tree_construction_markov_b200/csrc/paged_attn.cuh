@@ -5,7 +5,6 @@
 
 namespace dt {
 
-constexpr int kTcKeys = 128;        // cached positions of a key tile of the tensor-core kernel
 constexpr int kPagedSms = 148;      // the grids (and their workspace) are for at most this many SMs
 constexpr float kL2e = 1.4426950408889634f;
 
@@ -105,7 +104,7 @@ struct Cut {
 };
 
 // A row tile's units are those of the first tokens that stay visible, those
-// from the first to the last position that any of its rows sees, and one for
+// from the first to the last position that any of its rows sees, and those of
 // the tree's own rows.
 struct RowTile {
   int m0, live;     // its pairs [m0, m0 + live)
@@ -137,16 +136,14 @@ __device__ __forceinline__ RowTile row_tile(const PagedArgs& a, const PagedReque
   // (positions end below 2^30 and a unit has at most as many: no overflow)
   t.mains = t.hi > t.lo ? ((t.hi - 1) >> cut.shift) + 1 - t.first : 0;
   t.sinks = t.sink > 0 ? min(((t.sink - 1) >> cut.shift) + 1, t.first) : 0;
-  t.units = t.sinks + t.mains + (a.kt ? 1 : 0);
+  t.units = t.sinks + t.mains + (a.kt ? (q.n + (1 << cut.shift) - 1) >> cut.shift : 0);
   if (t.units == 0) t.units = t.mains = 1;  // nothing is seen: one unit, all of it masked
   return t;
 }
 
-// First position of unit u of a tile, or -1: the tree's rows.
-__device__ __forceinline__ int unit_base(const PagedArgs& a, const RowTile& t, int u, Cut cut) {
-  if (u < t.sinks) return u << cut.shift;
-  if (a.kt && u == t.units - 1) return -1;
-  return (t.first + u - t.sinks) << cut.shift;
+// First position of unit u of a chunk's tile.
+__device__ __forceinline__ int unit_base(const RowTile& t, int u, Cut cut) {
+  return (u < t.sinks ? u : t.first + u - t.sinks) << cut.shift;
 }
 
 // Does any row of the tile see a position of [s, s + n)?

@@ -103,10 +103,10 @@ struct Pieces {
 
   __device__ __forceinline__ void enter(const PagedArgs& a, Cut cut) {
     units = min(left, c.t.units - c.u);
-    open(a, cut);
+    open(cut);
   }
-  __device__ __forceinline__ void open(const PagedArgs& a, Cut cut) {
-    at = unit_base(a, c.t, c.u, cut);
+  __device__ __forceinline__ void open(Cut cut) {
+    at = unit_base(c.t, c.u, cut);
     // (a unit may be as long as all positions: the sum stays below 2^31)
     end = min(at + (1 << cut.shift), max(c.t.hi, c.t.sink));
   }
@@ -118,7 +118,7 @@ struct Pieces {
       --left;
       if (--units == 0) return false;
       ++c.u;
-      open(a, cut);
+      open(cut);
     }
   }
   // after find() was false: the next row tile; false: the share is done

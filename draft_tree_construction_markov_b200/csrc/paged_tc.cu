@@ -126,6 +126,11 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
                "r"(ok ? 16 : 0)
                : "memory");
 }
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(ok ? 4 : 0)
+               : "memory");
+}
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -167,9 +172,13 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
 struct RowMask {
   Visible vis;
   uint32_t tree[3];  // tree rows 0..64
-  // columns [32 w, 32 w + 32) of the tile at position `base` (-1: the tree's)
+  // columns [32 w, 32 w + 32) of the tile of KT keys at `base` (Item::base)
+  template <int KT>
   __device__ __forceinline__ uint32_t word(int base, int w) const {
-    if (base < 0) return w == 0 ? tree[0] : w == 1 ? tree[1] : w == 2 ? tree[2] : 0u;
+    if (base < 0) {
+      w += (-1 - base) * (KT / 32);
+      return w == 0 ? tree[0] : w == 1 ? tree[1] : w == 2 ? tree[2] : 0u;
+    }
     const int at = base + 32 * w;
     return low_bits(vis.last - at) & (~low_bits(vis.first - at) | low_bits(vis.sink - at));
   }
@@ -181,9 +190,11 @@ struct Item {
   int r0, n, len, p0;         // PagedRequest
   int u, seg, units, sinks;   // units [u, u + seg) of RowTile's
   int first, lo, hi, sink;
+  // first position of a unit; -1 - t: the tree's rows KT t, KT t + 1, ...
+  template <int KT>
   __device__ __forceinline__ int base(const PagedArgs& a, int unit) const {
-    return unit < sinks ? unit * kTcKeys
-                        : a.kt && unit == units - 1 ? -1 : (first + unit - sinks) * kTcKeys;
+    const int tree = a.kt ? unit - units + (n + KT - 1) / KT : -1;
+    return tree >= 0 ? -1 - tree : (unit < sinks ? unit : first + unit - sinks) * KT;
   }
   __device__ __forceinline__ bool seen(int s, int count) const {
     return (s < hi && s + count > lo) || s < sink;
@@ -195,21 +206,25 @@ template <int D, int CT, int NQ>
 struct TcShape {
   static constexpr bool kTma = CT == DT_BF16;
   static constexpr int KC = D / 64;
-  static constexpr int kChunk = 128 * 128;      // bytes of 128 rows x 64 bf16
-  static constexpr int kOperand = KC * kChunk;  // bytes of 128 rows x D
-  // key tiles in flight: a second one where shared memory has room for it
-  static constexpr int kStages = NQ == 2 || D == 64 ? 2 : 1;
-  static constexpr int kScales = 4;             // tiles of row scales (see the loader)
+  // positions of a key tile: 64 where two CTAs with their codes share an SM
+  static constexpr int KT = kTma || NQ == 2 ? 128 : 64, kShift = KT == 128 ? 7 : 6;
+  static constexpr int kQChunk = 128 * 128, kQTile = KC * kQChunk;  // 128 rows x 64 bf16, x D
+  static constexpr int kChunk = KT * 128, kTile = KC * kChunk;      // of keys or values
+  // key tiles in flight; codes have a ring of their own in front (half a tile: keys or values)
+  static constexpr int kStages = kTma && (NQ == 2 || D == 64) ? 2 : 1;
+  static constexpr int kCodes = 4, kCodeBytes = KT * D;
+  static constexpr int kScales = 4;             // tiles of slots and row scales (see the loader)
   // 32-column parts of S that a row keeps in registers between its two passes (bf16 caches)
   static constexpr int kKeep = NQ == 2 ? 4 : 2;
-  // Where shared memory or conversion leaves few registers, the warps come in
-  // whole warpgroups and deal them out anew: more for the softmax (S in
-  // registers), less for the others.  (A function call in the kernel would
-  // undo this: the compiler then allots the least of them to all.)
+  // Where registers are scarce the warps come in whole warpgroups and deal them
+  // out anew: more for the softmax (S in registers), less for the others.  (A
+  // function call in the kernel would undo this: the compiler then allots the
+  // least of them to all.  And nothing hot may spill: next to this much shared
+  // memory the L1 is too small for it.)
   static constexpr bool kDeal = NQ == 2 || !kTma;
-  static constexpr int kSoftRegs = kTma ? 200 : NQ == 2 ? 152 : 104;
-  static constexpr int kLoadRegs = kTma ? 104 : NQ == 2 ? 112 : 88;
-  static constexpr int kMmaRegs = kTma ? kLoadRegs : NQ == 2 ? 88 : 48;
+  static constexpr int kSoftRegs = kTma ? 200 : NQ == 2 ? 168 : 128;
+  static constexpr int kLoadRegs = kTma ? 104 : NQ == 2 ? 88 : 56;
+  static constexpr int kMmaRegs = kTma ? kLoadRegs : NQ == 2 ? 88 : 56;
   // registers a thread at launch (the most that the launch bounds leave), and
   // that the shares add up to no more
   static constexpr int kLaunchRegs = NQ == 1 ? 80 : kTma ? 168 : 128;
@@ -228,8 +243,12 @@ struct TcShape {
   static constexpr uint32_t kTmemCols = NQ == 2 ? 512 : 256;  // S: 128 columns a row tile, O: D
   static constexpr int kRows = 128 * NQ;
   static constexpr int kBars = 4 * kStages + 4 * NQ + kScales + 2 * kItems;
-  static constexpr size_t kSmem = (size_t)(NQ + 2 * kStages) * kOperand +
-                                  (kTma ? 0 : kScales * (3 * 128 * 4 + 16) + kSoft * sizeof(RowMask)) + kItems * sizeof(Item) + kBars * 8 + 16 + 1024;
+  static constexpr size_t kCoded = kTma ? 0
+                                        : (size_t)kCodes * kCodeBytes + kScales * (2 * KT * 4) +
+                                              kScales * 16 + kScales * KT * 4 +
+                                              kSoft * sizeof(RowMask);
+  static constexpr size_t kSmem = (size_t)NQ * kQTile + 2 * kStages * kTile + kCoded +
+                                  kItems * sizeof(Item) + kBars * 8 + 16 + 1024;
 };
 
 struct TcMaps {
@@ -241,17 +260,20 @@ template <int D, int CT, int NQ>
 __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, NQ>::kPerSm)
     paged_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ PagedArgs a) {
   using S = TcShape<D, CT, NQ>;
-  constexpr int KC = S::KC, ST = S::kStages;
+  constexpr int KC = S::KC, ST = S::kStages, KT = S::KT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* sq = smem;                              // Q [NQ][KC][128 rows][128 B]
-  uint8_t* sk = sq + NQ * S::kOperand;             // K [ST][KC][128 keys][128 B]
-  uint8_t* sv = sk + ST * S::kOperand;             // V [ST][KC][128 keys][128 B]
-  Item* items = (Item*)(sv + ST * S::kOperand);    // [kItems]
-  float* sscale = (float*)(items + S::kItems);     // [kScales][K, V][128]
-  int4* sinfo = (int4*)(sscale + (S::kTma ? 0 : S::kScales * 2 * 128));  // [kScales]
-  int* sslot = (int*)(sinfo + (S::kTma ? 0 : S::kScales));               // [kScales][128]
-  RowMask* smask = (RowMask*)(sslot + (S::kTma ? 0 : S::kScales * 128)); // [rows]
+  uint8_t* sk = sq + NQ * S::kQTile;               // K [ST][KC][KT keys][128 B]
+  uint8_t* sv = sk + ST * S::kTile;                // V [ST][KC][KT keys][128 B]
+  Item* items = (Item*)(sv + ST * S::kTile);       // [kItems]
+  // 8-bit caches: codes on their way, scales [K, V][KT] of a tile, {position,
+  // KV head, first row, rows} of a tile, slots of its positions; what each row sees
+  uint8_t* scode = (uint8_t*)(items + S::kItems);              // [kCodes][KT][D]
+  float* sscale = (float*)(scode + (S::kTma ? 0 : S::kCodes * S::kCodeBytes));
+  int4* sinfo = (int4*)(sscale + (S::kTma ? 0 : S::kScales * 2 * KT));
+  int* sslot = (int*)(sinfo + (S::kTma ? 0 : S::kScales));
+  RowMask* smask = (RowMask*)(sslot + (S::kTma ? 0 : S::kScales * KT));
   uint64_t* bars = (uint64_t*)(smask + (S::kTma ? 0 : S::kSoft));
   uint64_t* k_full = bars;
   uint64_t* k_empty = k_full + ST;
@@ -269,8 +291,7 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
   int64_t* sums = (int64_t*)(tslot + 4);           // [batch + 1]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr Cut cut = {S::kRows, 7};
-  static_assert(kTcKeys == 1 << 7);
+  constexpr Cut cut = {S::kRows, S::kShift};
   constexpr int kWarpMma = 4 * NQ, kWarpPlan = kWarpMma + 1;
   constexpr int kWarpLoad = S::kTma ? kWarpMma + 2 : (S::kSoft + S::kMma) / 32;
   pdl_launch_dependents();  // the join may be scheduled (it waits for this grid)
@@ -338,7 +359,7 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
         }
       } else if (warp == kWarpMma && lane == 0 && left > 0) {
         // ---------------------------------------------------------- the MMAs
-        constexpr uint32_t is = idesc_bf16_f32(128, 128);
+        constexpr uint32_t is = idesc_bf16_f32(128, KT);
         constexpr uint32_t io = idesc_bf16_f32(128, D) | (1u << 16);  // B is MN-major
         int ns = 0, np = 0;                  // key tiles whose S / O was issued
         uint32_t q_in = 0, p_in = 0;         // phases of q_full and p_full, a bit each
@@ -357,12 +378,12 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
             tc_fence_after();
           }
           if (!ok) return;
-          const uint32_t qa = desc_lo_k(smem_u32(sq) + q * S::kOperand);
-          const uint32_t ka = desc_lo_k(smem_u32(sk) + ns % ST * S::kOperand);
+          const uint32_t qa = desc_lo_k(smem_u32(sq) + q * S::kQTile);
+          const uint32_t ka = desc_lo_k(smem_u32(sk) + ns % ST * S::kTile);
 #pragma unroll
           for (int s = 0; s < 4 * KC; ++s) {
-            const uint32_t step = (s >> 2) * (S::kChunk >> 4) + (s & 3) * 2;
-            mma_ss(tmem + q * 128, qa + step, ka + step, is, s != 0);
+            mma_ss(tmem + q * 128, qa + (s >> 2) * (S::kQChunk >> 4) + (s & 3) * 2,
+                   ka + (s >> 2) * (S::kChunk >> 4) + (s & 3) * 2, is, s != 0);
           }
           tc_commit(&s_full[q]);
         };
@@ -373,7 +394,7 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
         for (int more = left; ok; --more) {
           const bool pv = live_q > 0, sc = more > 0;
           if (pv) ok = wait(&v_full[np % ST], (np / ST) & 1);
-          const uint32_t va = desc_lo_mn(smem_u32(sv) + np % ST * S::kOperand, S::kChunk);
+          const uint32_t va = desc_lo_mn(smem_u32(sv) + np % ST * S::kTile, S::kChunk);
 #pragma unroll 1
           for (int q = 0; q < NQ; ++q) {
             if (q < live_q) {
@@ -382,7 +403,7 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
               tc_fence_after();
               if (!ok) break;
 #pragma unroll
-              for (int s = 0; s < 8; ++s)
+              for (int s = 0; s < KT / 16; ++s)
                 mma_ts(tmem + NQ * 128 + q * D, tmem + q * 128 + 8 * s, va + 128 * s, io,
                        !first || s != 0);
               // (between tiles s_full of the next one says it: it tracks all products so far)
@@ -428,10 +449,10 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
           if (lane == 0) free_item(n);
           left -= it.seg;
           for (int u = it.u; u < it.u + it.seg && ok; ++u, ++g) {
-            const int base = it.base(a, u), st = g % ST;
+            const int base = it.template base<KT>(a, u), st = g % ST;
             const uint32_t parity = ((g / ST) & 1) ^ 1;
             int y = 0;
-            const bool mine = base < 0 ? lane == 0 : lane * box < kTcKeys;
+            const bool mine = base < 0 ? lane == 0 : lane * box < KT;
             if (base >= 0 && mine) {
               const int s = base + lane * box;
               // a piece that no row sees, or on a page that is none: out of bounds, read as zeros
@@ -441,7 +462,7 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
                                  : slot + ((int64_t)it.kvh << a.c.page_shift));
             }
             const uint32_t bytes =
-                base < 0 ? (uint32_t)(a.Nmax + 1) * D * 2 : (uint32_t)S::kOperand;
+                base < 0 ? (uint32_t)(a.Nmax + 1) * D * 2 : (uint32_t)S::kTile;
             auto load = [&](const CUtensorMap* cached, const CUtensorMap* tree, uint8_t* dst,
                             uint64_t* full, uint64_t* empty) {
               ok = __all_sync(0xffffffffu, ok && wait(empty, parity));
@@ -459,40 +480,41 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
               }
               __syncwarp();
             };
-            load(&maps.k, &maps.kt, sk + st * S::kOperand, &k_full[st], &k_empty[st]);
-            load(&maps.v, &maps.vt, sv + st * S::kOperand, &v_full[st], &v_empty[st]);
+            load(&maps.k, &maps.kt, sk + st * S::kTile, &k_full[st], &k_empty[st]);
+            load(&maps.v, &maps.vt, sv + st * S::kTile, &v_full[st], &v_empty[st]);
           }
         }
       } else if (left > 0) {
-        // 8-bit codes: a thread takes every 128th 16-byte piece of the tile.  The
-        // slots of a tile's positions (one a thread) are looked up two tiles ahead,
-        // its codes are in registers one tile ahead.
-        constexpr int kRowPieces = D / 16, kPieces = 128 * kRowPieces / 128;
+        // 8-bit codes: a thread takes every 128th 16-byte piece of a half tile x
+        // (keys of tile x / 2, or its values), from its copy into the ring of
+        // codes to its place as bf16.  Pages are looked up three tiles ahead,
+        // slots written down two ahead, codes and scales asked for three halves ahead.
+        constexpr int kRowPieces = D / 16, kPieces = KT * kRowPieces / 128;
+        constexpr int kStep = 128 / kRowPieces;  // rows from one of a thread's pieces to the next
         constexpr int kNone = INT_MIN;
         const int lt = tid - kWarpLoad * 32;
         const int piece = lt % kRowPieces, row0 = lt / kRowPieces;
-        uint4 kw[kPieces], vw[kPieces];
-        float kscale = 0.f, vscale = 0.f;
         int n = 0, u = 0;  // item and unit that look_up is at
         auto sync = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
         // page of this thread's position of the unit; kNone: not seen
         auto look_up = [&]() -> int {
           const Item& it = items[n % S::kItems];
-          const int s = it.base(a, u) + lt;
-          if (s < lt || !it.seen(s, 1)) return kNone;
+          const int base = it.template base<KT>(a, u), s = base + lt;
+          if (base < 0 || lt >= KT || !it.seen(s, 1)) return kNone;
           const int pi = s >> a.c.page_shift;
           return pi < a.c.max_pages ? __ldg(a.c.table + (int64_t)it.b * a.c.max_pages + pi) : -1;
         };
         // writes down its slot (-1: read as zeros), and goes on to the next unit
         auto plan = [&](int g, int page, bool more) {
           const Item& it = items[n % S::kItems];
-          const int base = it.base(a, u), at = (base + lt) & ((1 << a.c.page_shift) - 1);
+          const int base = it.template base<KT>(a, u);
+          const int at = (base + lt) & ((1 << a.c.page_shift) - 1);
           int slot = -1;
           if (page >= 0 && page < a.c.n_pages)
             slot = ((page * a.c.Hkv + it.kvh) << a.c.page_shift) + at;
           else if (page != kNone)
             set_status(a.status, DT_EDEVICE);
-          sslot[(g % S::kScales) * 128 + lt] = slot;
+          if (lt < KT) sslot[g % S::kScales * KT + lt] = slot;
           if (lt == 0) sinfo[g % S::kScales] = make_int4(base, it.kvh, it.r0, it.n);
           if (more && ++u == it.u + it.seg) {
             __syncwarp();
@@ -502,92 +524,100 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
             u = items[n % S::kItems].u;
           }
         };
-        auto fetch = [&](int g, const void* cache, const float* scales, uint4 (&w)[kPieces],
-                         float& scale) {
-          if (sinfo[g % S::kScales].x < 0) return;
-          const int* slots = sslot + (g % S::kScales) * 128;
+        // Asks for half x.  The scales' place was last used by tile x / 2 - 4: this
+        // comes after k_empty of tile x / 2 - 2, so S of the tile before that is
+        // complete, which was issued only after the softmax of tile x / 2 - 4.
+        auto ask = [&](int x) {
+          const int slot_at = (x >> 1) % S::kScales;
+          const int* slots = sslot + slot_at * KT;
+          float* scales = sscale + slot_at * 2 * KT;
+          if (sinfo[slot_at].x >= 0) {
+            const uint8_t* cache = (const uint8_t*)(x & 1 ? a.c.v : a.c.k) + piece * 16;
+            const uint32_t dst = smem_u32(scode + x % S::kCodes * S::kCodeBytes) + lt * 16;
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i) {
-            const int slot = slots[row0 + i * (128 / kRowPieces)];
-            w[i] = make_uint4(0, 0, 0, 0);
-            if (slot >= 0)
-              w[i] = __ldg((const uint4*)((const uint8_t*)cache + (int64_t)slot * D + piece * 16));
+            for (int i = 0; i < kPieces; ++i) {
+              const int slot = slots[row0 + i * kStep];
+              cp16(dst + i * 2048, cache + (int64_t)max(slot, 0) * D, slot >= 0);
+            }
+            if (!(x & 1)) {
+#pragma unroll
+              for (int i = lt; i < 2 * KT; i += 128) {
+                const int slot = slots[i % KT];
+                cp4(smem_u32(scales + i), (i < KT ? a.c.ks : a.c.vs) + max(slot, 0), slot >= 0);
+              }
+            }
+          } else if (!(x & 1)) {
+            for (int i = lt; i < 2 * KT; i += 128) scales[i] = 1.f;
           }
-          const int slot = slots[lt];
-          scale = slot < 0 ? 0.f : __ldg(scales + slot);
         };
-        // the tile into shared memory as bf16: codes that are in registers, or the tree's rows
-        auto place = [&](int g, uint8_t* dst, const void* tree, const uint4 (&w)[kPieces]) {
-          const int4 info = sinfo[g % S::kScales];
+        auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+        // The half x into its place.  The lanes of the second 64 columns store their
+        // 8-column halves in the other order, so that a quarter warp meets all 32
+        // banks; a thread's rows are a multiple of 8 apart: one swizzle for all.
+        const int c0 = (piece & 3) * 2, odd = piece >> 2;
+        const uint32_t at0 = odd * S::kChunk + sw128(row0, c0 + odd),
+                       at1 = odd * S::kChunk + sw128(row0, c0 + 1 - odd);
+        auto place = [&](int x) {
+          const int4 info = sinfo[(x >> 1) % S::kScales];
+          uint8_t* dst = x & 1 ? sv : sk;
           if (info.x < 0) {
-            const uint16_t* rows = (const uint16_t*)tree;
+            const uint16_t* rows = (const uint16_t*)(x & 1 ? a.vt : a.kt);
 #pragma unroll 2
-            for (int x = lt; x < 128 * KC * 8; x += 128) {
-              const int cc = x % (KC * 8), r = x / (KC * 8);
+            for (int y = lt; y < KT * KC * 8; y += 128) {
+              const int cc = y % (KC * 8), r = y / (KC * 8);
               uint4 v = make_uint4(0, 0, 0, 0);
-              if (r < info.w)
-                v = *(const uint4*)(rows + (((int64_t)info.z + r) * a.c.Hkv + info.y) * D + cc * 8);
+              const int at = (-1 - info.x) * KT + r;  // row of the tree
+              if (at < info.w)
+                v = *(const uint4*)(rows + (((int64_t)info.z + at) * a.c.Hkv + info.y) * D + cc * 8);
               *(uint4*)(dst + (cc >> 3) * S::kChunk + sw128(r, cc & 7)) = v;
             }
             return;
           }
-          // the lanes of the second 64 columns store their halves in the other order: all 32 banks
-          // (rows of a thread are 128 / kRowPieces apart, a multiple of 8: one swizzle for all)
-          const int c0 = (piece & 3) * 2, odd = piece >> 2;
-          uint8_t* at = dst + (piece >> 2) * S::kChunk;
-          uint8_t* at0 = at + sw128(row0, c0 + odd);
-          uint8_t* at1 = at + sw128(row0, c0 + 1 - odd);
-#pragma unroll
+          const uint8_t* src = scode + x % S::kCodes * S::kCodeBytes + lt * 16;
+#pragma unroll 2
           for (int i = 0; i < kPieces; ++i) {
+            const uint4 w = *(const uint4*)(src + i * 2048);
             uint32_t o[8];
-            const uint32_t in[4] = {odd ? w[i].z : w[i].x, odd ? w[i].w : w[i].y,
-                                    odd ? w[i].x : w[i].z, odd ? w[i].y : w[i].w};
+            const uint32_t in[4] = {odd ? w.z : w.x, odd ? w.w : w.y, odd ? w.x : w.z,
+                                    odd ? w.y : w.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) codes_to_bf16<CT>(in[e], o[2 * e], o[2 * e + 1]);
-            *(uint4*)(at0 + i * (128 / kRowPieces) * 128) = make_uint4(o[0], o[1], o[2], o[3]);
-            *(uint4*)(at1 + i * (128 / kRowPieces) * 128) = make_uint4(o[4], o[5], o[6], o[7]);
+            *(uint4*)(dst + at0 + i * kStep * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+            *(uint4*)(dst + at1 + i * kStep * 128) = make_uint4(o[4], o[5], o[6], o[7]);
           }
         };
+        static_assert(ST == 1 && S::kCodes == 4 && S::kScales == 4);
         ok = __all_sync(0xffffffffu, wait_item(0));
         u = items[0].u;
+        int ahead = kNone;
         if (ok) plan(0, look_up(), left > 1);
         if (ok && left > 1) plan(1, look_up(), left > 2);
+        if (ok && left > 2) ahead = look_up();
         sync();
-        if (ok) {
-          fetch(0, a.c.k, a.c.ks, kw, kscale);
-          fetch(0, a.c.v, a.c.vs, vw, vscale);
+        for (int x = 0; x < 3; ++x) {
+          if (ok && x < 2 * left) ask(x);
+          commit();
         }
-        for (int g = 0; left > 0; ++g, --left) {
-          const int st = g % ST;
-          const uint32_t parity = ((g / ST) & 1) ^ 1;
-          // (a warp that gives up goes on to the barriers, so that the others pass them)
-          int ahead = kNone;
-          if (ok && left > 2) ahead = look_up();
-          // The scales' slot was last used by tile g - 4.  k_empty means that S of
-          // tile g - ST is complete, which was issued only after the softmax of
-          // the tile before it had handed over P; so tile g - ST - 1 >= g - 4 is done.
-          float* scales = sscale + (g % S::kScales) * 256;
-          ok = __all_sync(0xffffffffu, ok && wait(&k_empty[st], parity));
-          if (ok) {
-            place(g, sk + st * S::kOperand, a.kt, kw);
-            const bool tree = sinfo[g % S::kScales].x < 0;
-            scales[lt] = tree ? 1.f : kscale;
-            scales[128 + lt] = tree ? 1.f : vscale;
-            fence_async_smem();
-            mbar_arrive(&k_full[st]);
-            mbar_arrive(&c_full[g % S::kScales]);
-            // the next tile's loads are on their way while this one is worked on
-            if (left > 1) fetch(g + 1, a.c.k, a.c.ks, kw, kscale);
-            ok = __all_sync(0xffffffffu, wait(&v_empty[st], parity));
+        // (a warp that gives up goes on to the barriers, so that the others pass them)
+#pragma unroll 1
+        for (int x = 0; x < 2 * left; ++x) {
+          const int g = x >> 1;
+          if (!(x & 1)) {
+            if (ok && g + 2 < left) plan(g + 2, ahead, g + 3 < left);
+            sync();
+            ahead = kNone;
+            if (ok && g + 3 < left) ahead = look_up();
           }
+          if (ok && x + 3 < 2 * left) ask(x + 3);
+          commit();
+          asm volatile("cp.async.wait_group 3;" ::: "memory");
+          ok = __all_sync(0xffffffffu, ok && wait(x & 1 ? v_empty : k_empty, (g & 1) ^ 1));
           if (ok) {
-            place(g, sv + st * S::kOperand, a.vt, vw);
+            place(x);
             fence_async_smem();
-            mbar_arrive(&v_full[st]);
-            if (left > 1) fetch(g + 1, a.c.v, a.c.vs, vw, vscale);
-            if (left > 2) plan(g + 2, ahead, left > 3);
+            mbar_arrive(x & 1 ? v_full : k_full);
+            if (!(x & 1)) mbar_arrive(&c_full[g % S::kScales]);
           }
-          sync();
         }
       }
     }
@@ -597,7 +627,7 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
     const int q = warp >> 2, row = tid & 127;
     const uint32_t quad = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + quad + q * 128, to = tmem + quad + NQ * 128 + q * D;
-    uint8_t* my_q = sq + q * S::kOperand;
+    uint8_t* my_q = sq + q * S::kQTile;
     const float sl2 = a.scale * kL2e;
     // item n's queries into shared memory, zeros where there is no row
     auto start_q = [&](int n) {
@@ -606,7 +636,7 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
 #pragma unroll 4
       for (int x = row; x < 128 * KC * 8; x += 128) {
         const int cc = x % (KC * 8), r = x / (KC * 8), m = m0 + (r < live ? r : 0);
-        cp16(smem_u32(my_q + (cc >> 3) * S::kChunk + sw128(r, cc & 7)),
+        cp16(smem_u32(my_q + (cc >> 3) * S::kQChunk + sw128(r, cc & 7)),
              (const uint16_t*)a.q + (r0 + (int64_t)(m / a.G)) * a.ld_q +
                  ((int64_t)h0 + m % a.G) * D + cc * 8,
              r < live);
@@ -675,8 +705,8 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
         }
       };
       for (int k = 0; k < seg; ++k, ++g, ++n_done) {
-        const int base = it.base(a, it.u + k);
-        const bool masked = base < whole_lo || base + kTcKeys > whole_hi;
+        const int base = it.template base<KT>(a, it.u + k);
+        const bool masked = base < whole_lo || base + KT > whole_hi;
         ok = wait(&s_full[q], n_done & 1);
         if constexpr (!S::kTma)
           ok = ok && wait(&c_full[g % S::kScales], (g / S::kScales) & 1);
@@ -701,7 +731,7 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
             if (masked) {
 #pragma unroll
               for (int w = w0; w < w0 + kKeep; ++w) {
-                const uint32_t see = mask.word(base, w);
+                const uint32_t see = mask.template word<KT>(base, w);
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
                   r[w - w0][e] = (see >> e) & 1u ? r[w - w0][e] : 0xff800000u;
@@ -756,10 +786,10 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
           l += (la[0] + la[1]) + (la[2] + la[3]);
           // V rows that are no positions of the request may hold anything: zeros, before 0 * NaN
           const int valid = base < 0 ? rq.n : rq.len - base;
-          if (valid < kTcKeys) {
+          if (valid < KT) {
             ok = __all_sync(0xffffffffu, wait(&v_full[g % ST], (g / ST) & 1));
             if (!ok) break;
-            uint8_t* v = sv + (g % ST) * S::kOperand;
+            uint8_t* v = sv + (g % ST) * S::kTile;
 #pragma unroll 1
             for (int x = row; x < 128 * KC * 8; x += 128) {
               const int r8 = x / (KC * 8), cc = x % (KC * 8);
@@ -774,7 +804,7 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
           // In fragment layout a lane has a quarter of the columns of four rows.
           // (A scale of NaN at a place that a row does not see makes its sum NaN,
           // with a finite weight sum: such rows are done again, see paged_row.)
-          const float* kscale = sscale + (g % S::kScales) * 256 + 2 * (lane & 3);
+          const float* kscale = sscale + (g % S::kScales) * 2 * KT + 2 * (lane & 3);
           const RowMask* rows = smask + q * 128 + 32 * (warp & 3) + (lane >> 2);
           uint32_t r[2][32];  // 64 columns of rows lane / 4 + 0, 8 and + 16, 24
           // scores of half hh: times the keys' scales, -infinity where the row does not see
@@ -794,7 +824,7 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
               for (int x = 0; x < 4; ++x)
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                  const uint32_t see = rows[8 * x].word(base, 2 * hh + y) >> (2 * (lane & 3));
+                  const uint32_t see = rows[8 * x].template word<KT>(base, 2 * hh + y) >> (2 * (lane & 3));
 #pragma unroll
                   for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -807,7 +837,7 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
           };
           float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int hh = 1; hh >= 0; --hh) {
+          for (int hh = KT / 64 - 1; hh >= 0; --hh) {
             load(hh);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -843,14 +873,14 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
 #pragma unroll
           for (int x = 0; x < 4; ++x) less[x] = m4[x] == -INFINITY ? 0.f : -m4[x];
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
+          for (int hh = 0; hh < KT / 64; ++hh) {
             if (hh) load(hh);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               uint32_t pk[16];
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
-                const float2 f = *(const float2*)(kscale + 128 + 64 * hh + 8 * j);
+                const float2 f = *(const float2*)(kscale + KT + 64 * hh + 8 * j);
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
                   const int x = 2 * t + z;
@@ -970,7 +1000,7 @@ cudaError_t launch_shape(const PagedArgs& a, const TcMaps& maps, int ctas, cudaS
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  return launch_paged_join(a, CT, Cut{S::kRows, 7}, ctas, s);
+  return launch_paged_join(a, CT, Cut{S::kRows, S::kShift}, ctas, s);
 }
 
 }  // namespace
