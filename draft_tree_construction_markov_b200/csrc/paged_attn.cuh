@@ -286,6 +286,16 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
+// Contiguous bytes (16-byte aligned, a multiple of 16) into shared memory.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // Weight sum of a row -> the factor of its output: 0 where the row sees
 // nothing; 1 / 0 (so that 0 * inf = NaN) where all it sees is -infinity.
 __device__ __forceinline__ float row_factor(float l, bool sees) { return sees ? 1.f / l : 0.f; }

@@ -24,8 +24,6 @@
 // The work of a call (row tiles x KV heads x key tiles) is divided over the
 // CTAs in equal consecutive shares; a row tile that two shares cut is joined by
 // paged_join_kernel from fp32 partials.
-#include <limits.h>
-
 #include <algorithm>
 #include <type_traits>
 
@@ -126,11 +124,6 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
                "r"(ok ? 16 : 0)
                : "memory");
 }
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
-               "r"(ok ? 4 : 0)
-               : "memory");
-}
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -213,7 +206,7 @@ struct TcShape {
   // key tiles in flight; codes have a ring of their own in front (half a tile: keys or values)
   static constexpr int kStages = kTma && (NQ == 2 || D == 64) ? 2 : 1;
   static constexpr int kCodes = 4, kCodeBytes = KT * D;
-  static constexpr int kScales = 4;             // tiles of slots and row scales (see the loader)
+  static constexpr int kScales = 4;             // tiles of row scales (see the loader)
   // 32-column parts of S that a row keeps in registers between its two passes (bf16 caches)
   static constexpr int kKeep = NQ == 2 ? 4 : 2;
   // Where registers are scarce the warps come in whole warpgroups and deal them
@@ -232,27 +225,25 @@ struct TcShape {
                                 : 2 * kSoftRegs + kLoadRegs + kMmaRegs <= 4 * kLaunchRegs)
                         : kTma || kSoftRegs + kLoadRegs + kMmaRegs <= 3 * kLaunchRegs);
   static constexpr int kSoft = 128 * NQ;
-  // warps of the MMAs, of the schedule, of a TMA loader, and idle ones that fill a warpgroup;
-  // the loaders of codes are a warpgroup of their own
+  // warps of the MMAs, of the schedule, of TMA, and idle ones that fill a warpgroup; what turns
+  // codes into bf16 is a warpgroup of its own
   static constexpr int kMma = kDeal ? 128 : 96;
   static constexpr int kLoad = kTma ? 0 : 128;
-  static constexpr int kLoadWarps = kTma ? 1 : 4;
+  static constexpr int kItemUsers = 2 + 4 * NQ + kLoad / 32;  // MMAs, TMA, softmax, codes
   static constexpr int kThreads = kSoft + kMma + kLoad;
   static constexpr int kItems = 4;  // row tiles that the schedule is ahead
   static constexpr int kPerSm = NQ == 2 ? 1 : 2;
   static constexpr uint32_t kTmemCols = NQ == 2 ? 512 : 256;  // S: 128 columns a row tile, O: D
   static constexpr int kRows = 128 * NQ;
-  static constexpr int kBars = 4 * kStages + 4 * NQ + kScales + 2 * kItems;
-  static constexpr size_t kCoded = kTma ? 0
-                                        : (size_t)kCodes * kCodeBytes + kScales * (2 * KT * 4) +
-                                              kScales * 16 + kScales * KT * 4 +
-                                              kSoft * sizeof(RowMask);
+  static constexpr int kBars = 4 * kStages + 4 * NQ + kScales + 2 * kCodes + 2 * kItems;
+  static constexpr size_t kCoded =
+      kTma ? 0 : (size_t)kCodes * kCodeBytes + kScales * (2 * KT * 4) + kSoft * 16;
   static constexpr size_t kSmem = (size_t)NQ * kQTile + 2 * kStages * kTile + kCoded +
                                   kItems * sizeof(Item) + kBars * 8 + 16 + 1024;
 };
 
 struct TcMaps {
-  CUtensorMap k, v;    // the cache, [slots][D], boxes of 64 x min(page, 128)
+  CUtensorMap k, v;    // the cache, [slots][D], boxes of min(D, 128 bytes) x min(page, key tile)
   CUtensorMap kt, vt;  // the tree's rows, [rows][Hkv * D], boxes of 64 x (Nmax + 1)
 };
 
@@ -266,15 +257,12 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
   uint8_t* sq = smem;                              // Q [NQ][KC][128 rows][128 B]
   uint8_t* sk = sq + NQ * S::kQTile;               // K [ST][KC][KT keys][128 B]
   uint8_t* sv = sk + ST * S::kTile;                // V [ST][KC][KT keys][128 B]
-  Item* items = (Item*)(sv + ST * S::kTile);       // [kItems]
-  // 8-bit caches: codes on their way, scales [K, V][KT] of a tile, {position,
-  // KV head, first row, rows} of a tile, slots of its positions; what each row sees
-  uint8_t* scode = (uint8_t*)(items + S::kItems);              // [kCodes][KT][D]
-  float* sscale = (float*)(scode + (S::kTma ? 0 : S::kCodes * S::kCodeBytes));
-  int4* sinfo = (int4*)(sscale + (S::kTma ? 0 : S::kScales * 2 * KT));
-  int* sslot = (int*)(sinfo + (S::kTma ? 0 : S::kScales));
-  RowMask* smask = (RowMask*)(sslot + (S::kTma ? 0 : S::kScales * KT));
-  uint64_t* bars = (uint64_t*)(smask + (S::kTma ? 0 : S::kSoft));
+  // 8-bit caches: halves of tiles (keys, values) as codes, scales of tiles, what each row sees
+  uint8_t* scode = (uint8_t*)(sv + ST * S::kTile);                       // [kCodes][KT][D]
+  float* sscale = (float*)(scode + (S::kTma ? 0 : S::kCodes * S::kCodeBytes));  // [kScales][K, V][KT]
+  uint4* smask = (uint4*)(sscale + (S::kTma ? 0 : S::kScales * 2 * KT));        // [rows]
+  Item* items = (Item*)(smask + (S::kTma ? 0 : S::kSoft));               // [kItems]
+  uint64_t* bars = (uint64_t*)(items + S::kItems);
   uint64_t* k_full = bars;
   uint64_t* k_empty = k_full + ST;
   uint64_t* v_full = k_empty + ST;
@@ -284,7 +272,9 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
   uint64_t* p_full = s_full + NQ;
   uint64_t* o_full = p_full + NQ;
   uint64_t* c_full = o_full + NQ;                  // the scales of a tile are there
-  uint64_t* i_full = c_full + S::kScales;          // an item is there
+  uint64_t* w_full = c_full + S::kScales;          // a half's codes are there
+  uint64_t* w_empty = w_full + S::kCodes;
+  uint64_t* i_full = w_empty + S::kCodes;          // an item is there
   uint64_t* i_empty = i_full + S::kItems;
   uint32_t* tslot = (uint32_t*)(i_empty + S::kItems);
   volatile int* abort_flag = (volatile int*)(tslot + 1);
@@ -293,7 +283,7 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr Cut cut = {S::kRows, S::kShift};
   constexpr int kWarpMma = 4 * NQ, kWarpPlan = kWarpMma + 1;
-  constexpr int kWarpLoad = S::kTma ? kWarpMma + 2 : (S::kSoft + S::kMma) / 32;
+  constexpr int kWarpTma = kWarpMma + 2, kWarpLoad = kWarpMma + S::kMma / 32;
   pdl_launch_dependents();  // the join may be scheduled (it waits for this grid)
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
@@ -311,7 +301,11 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
     for (int i = 0; i < S::kScales; ++i) mbar_init(&c_full[i], 128);
     for (int i = 0; i < S::kItems; ++i) {
       mbar_init(&i_full[i], 1);
-      mbar_init(&i_empty[i], 1 + S::kLoadWarps + 4 * NQ);
+      mbar_init(&i_empty[i], S::kItemUsers);
+    }
+    for (int i = 0; i < S::kCodes; ++i) {
+      mbar_init(&w_full[i], 1);
+      mbar_init(&w_empty[i], 4);
     }
     *abort_flag = 0;
     a.redo[blockIdx.x] = 0;
@@ -339,7 +333,7 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
   // once the others have been lowered.
   if (warp >= kWarpMma) {
     if constexpr (S::kDeal && S::kTma) deal_regs<S::kLaunchRegs, S::kLoadRegs>();
-    if (warp < kWarpMma + S::kMma / 32 && !(S::kTma && warp == kWarpLoad)) {
+    if (warp < kWarpLoad) {
       if constexpr (S::kDeal && !S::kTma) deal_regs<S::kLaunchRegs, S::kMmaRegs>();
       if (warp == kWarpPlan && lane == 0 && left > 0) {
         // ------------------------------------------------------ the schedule
@@ -433,192 +427,161 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
             live_next = pairs;
           }
         }
-      }
-    } else {
-      // -------------------------------------------------------------- the loads
-      if constexpr (S::kDeal && !S::kTma) deal_regs<S::kLaunchRegs, S::kLoadRegs>();
-      bool ok = true;
-      if constexpr (S::kTma) {
-        const int page = 1 << a.c.page_shift, box = min(page, 128);
+      } else if (warp == kWarpTma) {
+        // ------------------------------------------------------------- copies
+        // bf16: into the operands' places; codes: half a tile at a time into
+        // their ring, with the tile's scales beside the keys
+        const int page = 1 << a.c.page_shift, box = min(page, KT);
+        bool ok = true;
         int g = 0;
         for (int n = 0; left > 0 && ok; ++n) {
           ok = __all_sync(0xffffffffu, wait_item(n));
           if (!ok) break;
-          const Item it = items[n % S::kItems];
-          __syncwarp();
-          if (lane == 0) free_item(n);
+          const Item& it = items[n % S::kItems];
           left -= it.seg;
-          for (int u = it.u; u < it.u + it.seg && ok; ++u, ++g) {
-            const int base = it.template base<KT>(a, u), st = g % ST;
-            const uint32_t parity = ((g / ST) & 1) ^ 1;
-            int y = 0;
+          for (int k = 0; k < it.seg && ok; ++k, ++g) {
+            const int base = it.template base<KT>(a, it.u + k);
             const bool mine = base < 0 ? lane == 0 : lane * box < KT;
-            if (base >= 0 && mine) {
-              const int s = base + lane * box;
-              // a piece that no row sees, or on a page that is none: out of bounds, read as zeros
-              int64_t slot = -1;
-              if (it.seen(s, box)) slot = a.c.slot(it.b, s, a.status);
-              y = (int)(slot < 0 ? ((int64_t)a.c.n_pages * a.c.Hkv) << a.c.page_shift
-                                 : slot + ((int64_t)it.kvh << a.c.page_shift));
+            // a piece that no row sees, or on a page that is none: out of bounds, read as zeros
+            int slot = -1;
+            if (base >= 0 && mine && it.seen(base + lane * box, box)) {
+              const int64_t at = a.c.slot(it.b, base + lane * box, a.status);
+              if (at >= 0) slot = (int)(at + ((int64_t)it.kvh << a.c.page_shift));
             }
-            const uint32_t bytes =
-                base < 0 ? (uint32_t)(a.Nmax + 1) * D * 2 : (uint32_t)S::kTile;
-            auto load = [&](const CUtensorMap* cached, const CUtensorMap* tree, uint8_t* dst,
-                            uint64_t* full, uint64_t* empty) {
-              ok = __all_sync(0xffffffffu, ok && wait(empty, parity));
-              if (!ok) return;
-              if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-              __syncwarp();
-              if (mine) {
+            const int y = slot >= 0 ? slot : (int)(((int64_t)a.c.n_pages * a.c.Hkv) << a.c.page_shift);
+#pragma unroll 1
+            for (int part = 0; part < 2 && ok; ++part) {
+              const CUtensorMap* map = part ? &maps.v : &maps.k;
+              if constexpr (S::kTma) {
+                const int st = g % ST;
+                uint64_t* full = (part ? v_full : k_full) + st;
+                uint8_t* dst = (part ? sv : sk) + st * S::kTile;
+                ok = __all_sync(0xffffffffu, wait((part ? v_empty : k_empty) + st, ((g / ST) & 1) ^ 1));
+                if (!ok) break;
+                if (lane == 0)
+                  mbar_arrive_expect_tx(full, base < 0 ? (uint32_t)(a.Nmax + 1) * D * 2
+                                                       : (uint32_t)S::kTile);
+                __syncwarp();
+                if (mine) {
 #pragma unroll
-                for (int kc = 0; kc < KC; ++kc) {
-                  if (base < 0)
-                    tma_load_2d(dst + kc * S::kChunk, tree, full, it.kvh * D + kc * 64, it.r0);
-                  else
-                    tma_load_2d(dst + kc * S::kChunk + lane * box * 128, cached, full, kc * 64, y);
+                  for (int kc = 0; kc < KC; ++kc) {
+                    if (base < 0)
+                      tma_load_2d(dst + kc * S::kChunk, part ? &maps.vt : &maps.kt, full,
+                                  it.kvh * D + kc * 64, it.r0);
+                    else
+                      tma_load_2d(dst + kc * S::kChunk + lane * box * 128, map, full, kc * 64, y);
+                  }
+                }
+              } else {
+                const int x = 2 * g + part, st = x % S::kCodes;
+                float* scales = sscale + (g % S::kScales) * 2 * KT;
+                // The scales' place was last used by tile g - 4.  The ring's (w_empty) was
+                // emptied by half x - 4, and before its codes were turned the one before it,
+                // which had waited for the keys' or values' place: P of tile g - 4 was there.
+                ok = __all_sync(0xffffffffu, wait(&w_empty[st], ((x / S::kCodes) & 1) ^ 1));
+                if (!ok) break;
+                if (base < 0) {  // the tree's rows come as bf16, without scales
+                  if (part == 0)
+                    for (int i = lane; i < 2 * KT; i += 32) scales[i] = 1.f;
+                  fence_async_smem();
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive(&w_full[st]);
+                } else {
+                  const unsigned there = __ballot_sync(0xffffffffu, mine && slot >= 0);
+                  if (part == 0 && mine && slot < 0) {
+                    for (int i = 0; i < box; ++i)
+                      scales[lane * box + i] = scales[KT + lane * box + i] = 0.f;
+                    fence_async_smem();
+                  }
+                  __syncwarp();
+                  if (lane == 0)
+                    mbar_arrive_expect_tx(&w_full[st], S::kCodeBytes +
+                                                           (part ? 0 : __popc(there) * box * 8));
+                  __syncwarp();
+                  if (mine) {
+                    tma_load_2d(scode + st * S::kCodeBytes + lane * box * D, map, &w_full[st], 0, y);
+                    if (part == 0 && slot >= 0) {
+                      bulk_load(scales + lane * box, a.c.ks + slot, box * 4, &w_full[st]);
+                      bulk_load(scales + KT + lane * box, a.c.vs + slot, box * 4, &w_full[st]);
+                    }
+                  }
                 }
               }
               __syncwarp();
-            };
-            load(&maps.k, &maps.kt, sk + st * S::kTile, &k_full[st], &k_empty[st]);
-            load(&maps.v, &maps.vt, sv + st * S::kTile, &v_full[st], &v_empty[st]);
-          }
-        }
-      } else if (left > 0) {
-        // 8-bit codes: a thread takes every 128th 16-byte piece of a half tile x
-        // (keys of tile x / 2, or its values), from its copy into the ring of
-        // codes to its place as bf16.  Pages are looked up three tiles ahead,
-        // slots written down two ahead, codes and scales asked for three halves ahead.
-        constexpr int kRowPieces = D / 16, kPieces = KT * kRowPieces / 128;
-        constexpr int kStep = 128 / kRowPieces;  // rows from one of a thread's pieces to the next
-        constexpr int kNone = INT_MIN;
-        const int lt = tid - kWarpLoad * 32;
-        const int piece = lt % kRowPieces, row0 = lt / kRowPieces;
-        int n = 0, u = 0;  // item and unit that look_up is at
-        auto sync = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
-        // page of this thread's position of the unit; kNone: not seen
-        auto look_up = [&]() -> int {
-          const Item& it = items[n % S::kItems];
-          const int base = it.template base<KT>(a, u), s = base + lt;
-          if (base < 0 || lt >= KT || !it.seen(s, 1)) return kNone;
-          const int pi = s >> a.c.page_shift;
-          return pi < a.c.max_pages ? __ldg(a.c.table + (int64_t)it.b * a.c.max_pages + pi) : -1;
-        };
-        // writes down its slot (-1: read as zeros), and goes on to the next unit
-        auto plan = [&](int g, int page, bool more) {
-          const Item& it = items[n % S::kItems];
-          const int base = it.template base<KT>(a, u);
-          const int at = (base + lt) & ((1 << a.c.page_shift) - 1);
-          int slot = -1;
-          if (page >= 0 && page < a.c.n_pages)
-            slot = ((page * a.c.Hkv + it.kvh) << a.c.page_shift) + at;
-          else if (page != kNone)
-            set_status(a.status, DT_EDEVICE);
-          if (lt < KT) sslot[g % S::kScales * KT + lt] = slot;
-          if (lt == 0) sinfo[g % S::kScales] = make_int4(base, it.kvh, it.r0, it.n);
-          if (more && ++u == it.u + it.seg) {
-            __syncwarp();
-            if (lane == 0) free_item(n);
-            ++n;
-            ok = __all_sync(0xffffffffu, ok && wait_item(n));
-            u = items[n % S::kItems].u;
-          }
-        };
-        // Asks for half x.  The scales' place was last used by tile x / 2 - 4: this
-        // comes after k_empty of tile x / 2 - 2, so S of the tile before that is
-        // complete, which was issued only after the softmax of tile x / 2 - 4.
-        auto ask = [&](int x) {
-          const int slot_at = (x >> 1) % S::kScales;
-          const int* slots = sslot + slot_at * KT;
-          float* scales = sscale + slot_at * 2 * KT;
-          if (sinfo[slot_at].x >= 0) {
-            const uint8_t* cache = (const uint8_t*)(x & 1 ? a.c.v : a.c.k) + piece * 16;
-            const uint32_t dst = smem_u32(scode + x % S::kCodes * S::kCodeBytes) + lt * 16;
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-              const int slot = slots[row0 + i * kStep];
-              cp16(dst + i * 2048, cache + (int64_t)max(slot, 0) * D, slot >= 0);
             }
-            if (!(x & 1)) {
+          }
+          __syncwarp();
+          if (lane == 0) free_item(n);
+        }
+      }
+    } else if constexpr (!S::kTma) {
+      // ---------------------------------------------------- codes into operands
+      // A thread turns every 128th 16-byte piece of a half tile into bf16.  Eight
+      // lanes take the same columns of eight neighbouring rows, in which the
+      // swizzles of both rings put them into different banks.
+      deal_regs<S::kLaunchRegs, S::kLoadRegs>();
+      constexpr int kRowPieces = D / 16, kPieces = KT * kRowPieces / 128;
+      constexpr int kStep = 128 / kRowPieces;  // rows from one of a thread's pieces to the next
+      const int lw = warp - kWarpLoad;
+      const int piece = (lane >> 3) + (D == 128 ? 4 * (lw & 1) : 0);
+      const int row0 = (lane & 7) + 8 * (D == 128 ? lw >> 1 : lw);
+      const uint32_t from = row0 * D + (D == 128 ? (piece ^ (row0 & 7)) << 4
+                                                 : (piece ^ ((row0 >> 1) & 3)) << 4);
+      const uint32_t to0 = (piece >> 2) * S::kChunk + sw128(row0, (piece & 3) * 2),
+                     to1 = (piece >> 2) * S::kChunk + sw128(row0, (piece & 3) * 2 + 1);
+      static_assert(ST == 1 && S::kScales == 4 && S::kCodes == 4);
+      bool ok = true;
+      int g = 0;
+      for (int n = 0; left > 0 && ok; ++n) {
+        ok = __all_sync(0xffffffffu, wait_item(n));
+        if (!ok) break;
+        const Item& it = items[n % S::kItems];
+        left -= it.seg;
+        for (int k = 0; k < it.seg && ok; ++k, ++g) {
+          const int base = it.template base<KT>(a, it.u + k);
+#pragma unroll 1
+          for (int part = 0; part < 2; ++part) {
+            const int x = 2 * g + part, st = x % S::kCodes;
+            uint8_t* dst = part ? sv : sk;
+            ok = __all_sync(0xffffffffu, wait(&w_full[st], (x / S::kCodes) & 1));
+            if (!ok) break;
+            uint4 w[kPieces];
 #pragma unroll
-              for (int i = lt; i < 2 * KT; i += 128) {
-                const int slot = slots[i % KT];
-                cp4(smem_u32(scales + i), (i < KT ? a.c.ks : a.c.vs) + max(slot, 0), slot >= 0);
+            for (int i = 0; i < kPieces; ++i)
+              w[i] = *(const uint4*)(scode + st * S::kCodeBytes + from + i * kStep * D);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&w_empty[st]);
+            ok = __all_sync(0xffffffffu, wait(part ? v_empty : k_empty, (g & 1) ^ 1));
+            if (!ok) break;
+            if (base >= 0) {
+#pragma unroll
+              for (int i = 0; i < kPieces; ++i) {
+                uint32_t o[8];
+                codes_to_bf16<CT>(w[i].x, o[0], o[1]);
+                codes_to_bf16<CT>(w[i].y, o[2], o[3]);
+                codes_to_bf16<CT>(w[i].z, o[4], o[5]);
+                codes_to_bf16<CT>(w[i].w, o[6], o[7]);
+                *(uint4*)(dst + to0 + i * kStep * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+                *(uint4*)(dst + to1 + i * kStep * 128) = make_uint4(o[4], o[5], o[6], o[7]);
+              }
+            } else {
+              const uint16_t* rows = (const uint16_t*)(part ? a.vt : a.kt);
+#pragma unroll 2
+              for (int y = tid & 127; y < KT * KC * 8; y += 128) {
+                const int cc = y % (KC * 8), r = y / (KC * 8), at = (-1 - base) * KT + r;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (at < it.n)
+                  v = *(const uint4*)(rows + (((int64_t)it.r0 + at) * a.c.Hkv + it.kvh) * D + cc * 8);
+                *(uint4*)(dst + (cc >> 3) * S::kChunk + sw128(r, cc & 7)) = v;
               }
             }
-          } else if (!(x & 1)) {
-            for (int i = lt; i < 2 * KT; i += 128) scales[i] = 1.f;
-          }
-        };
-        auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
-        // The half x into its place.  The lanes of the second 64 columns store their
-        // 8-column halves in the other order, so that a quarter warp meets all 32
-        // banks; a thread's rows are a multiple of 8 apart: one swizzle for all.
-        const int c0 = (piece & 3) * 2, odd = piece >> 2;
-        const uint32_t at0 = odd * S::kChunk + sw128(row0, c0 + odd),
-                       at1 = odd * S::kChunk + sw128(row0, c0 + 1 - odd);
-        auto place = [&](int x) {
-          const int4 info = sinfo[(x >> 1) % S::kScales];
-          uint8_t* dst = x & 1 ? sv : sk;
-          if (info.x < 0) {
-            const uint16_t* rows = (const uint16_t*)(x & 1 ? a.vt : a.kt);
-#pragma unroll 2
-            for (int y = lt; y < KT * KC * 8; y += 128) {
-              const int cc = y % (KC * 8), r = y / (KC * 8);
-              uint4 v = make_uint4(0, 0, 0, 0);
-              const int at = (-1 - info.x) * KT + r;  // row of the tree
-              if (at < info.w)
-                v = *(const uint4*)(rows + (((int64_t)info.z + at) * a.c.Hkv + info.y) * D + cc * 8);
-              *(uint4*)(dst + (cc >> 3) * S::kChunk + sw128(r, cc & 7)) = v;
-            }
-            return;
-          }
-          const uint8_t* src = scode + x % S::kCodes * S::kCodeBytes + lt * 16;
-#pragma unroll 2
-          for (int i = 0; i < kPieces; ++i) {
-            const uint4 w = *(const uint4*)(src + i * 2048);
-            uint32_t o[8];
-            const uint32_t in[4] = {odd ? w.z : w.x, odd ? w.w : w.y, odd ? w.x : w.z,
-                                    odd ? w.y : w.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) codes_to_bf16<CT>(in[e], o[2 * e], o[2 * e + 1]);
-            *(uint4*)(dst + at0 + i * kStep * 128) = make_uint4(o[0], o[1], o[2], o[3]);
-            *(uint4*)(dst + at1 + i * kStep * 128) = make_uint4(o[4], o[5], o[6], o[7]);
-          }
-        };
-        static_assert(ST == 1 && S::kCodes == 4 && S::kScales == 4);
-        ok = __all_sync(0xffffffffu, wait_item(0));
-        u = items[0].u;
-        int ahead = kNone;
-        if (ok) plan(0, look_up(), left > 1);
-        if (ok && left > 1) plan(1, look_up(), left > 2);
-        if (ok && left > 2) ahead = look_up();
-        sync();
-        for (int x = 0; x < 3; ++x) {
-          if (ok && x < 2 * left) ask(x);
-          commit();
-        }
-        // (a warp that gives up goes on to the barriers, so that the others pass them)
-#pragma unroll 1
-        for (int x = 0; x < 2 * left; ++x) {
-          const int g = x >> 1;
-          if (!(x & 1)) {
-            if (ok && g + 2 < left) plan(g + 2, ahead, g + 3 < left);
-            sync();
-            ahead = kNone;
-            if (ok && g + 3 < left) ahead = look_up();
-          }
-          if (ok && x + 3 < 2 * left) ask(x + 3);
-          commit();
-          asm volatile("cp.async.wait_group 3;" ::: "memory");
-          ok = __all_sync(0xffffffffu, ok && wait(x & 1 ? v_empty : k_empty, (g & 1) ^ 1));
-          if (ok) {
-            place(x);
             fence_async_smem();
-            mbar_arrive(x & 1 ? v_full : k_full);
-            if (!(x & 1)) mbar_arrive(&c_full[g % S::kScales]);
+            mbar_arrive(part ? v_full : k_full);
+            if (part == 0) mbar_arrive(&c_full[g % S::kScales]);
           }
         }
+        __syncwarp();
+        if (lane == 0) free_item(n);
       }
     }
   } else {
@@ -682,10 +645,6 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
         mask.tree[2] = (uint32_t)(anc >> 63) & low_bits(rq.n - 64);
       }
       const bool sees = a.kt || mask.vis.sink > 0 || mask.vis.last > mask.vis.first;
-      if constexpr (!S::kTma) {
-        smask[q * 128 + row] = mask;
-        __syncwarp();
-      }
       // key tiles in [whole_lo, whole_hi) need no mask for any row of the warp
       const int whole_lo = __reduce_max_sync(0xffffffffu, mask.vis.first);
       const int whole_hi = __reduce_min_sync(0xffffffffu, mask.vis.last);
@@ -805,7 +764,15 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
           // (A scale of NaN at a place that a row does not see makes its sum NaN,
           // with a finite weight sum: such rows are done again, see paged_row.)
           const float* kscale = sscale + (g % S::kScales) * 2 * KT + 2 * (lane & 3);
-          const RowMask* rows = smask + q * 128 + 32 * (warp & 3) + (lane >> 2);
+          const uint4* rows = smask + q * 128 + 32 * (warp & 3) + (lane >> 2);
+          if (masked) {  // what each row sees of this tile, by the thread that has it
+            uint32_t w[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) w[y] = y < KT / 32 ? mask.template word<KT>(base, y) : 0u;
+            __syncwarp();
+            smask[q * 128 + row] = make_uint4(w[0], w[1], w[2], w[3]);
+            __syncwarp();
+          }
           uint32_t r[2][32];  // 64 columns of rows lane / 4 + 0, 8 and + 16, 24
           // scores of half hh: times the keys' scales, -infinity where the row does not see
           auto load = [&](int hh) {
@@ -821,18 +788,17 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
             }
             if (masked) {
 #pragma unroll
-              for (int x = 0; x < 4; ++x)
+              for (int x = 0; x < 4; ++x) {
+                const uint2 two = ((const uint2*)(rows + 8 * x))[hh];
+                const uint32_t see[2] = {two.x >> (2 * (lane & 3)), two.y >> (2 * (lane & 3))};
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                  const uint32_t see = rows[8 * x].template word<KT>(base, 2 * hh + y) >> (2 * (lane & 3));
+                for (int j = 0; j < 8; ++j)
 #pragma unroll
-                  for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                      uint32_t& z = r[x >> 1][4 * (4 * y + j) + 2 * (x & 1) + e];
-                      z = (see >> (8 * j + e)) & 1u ? z : 0xff800000u;
-                    }
-                }
+                  for (int e = 0; e < 2; ++e) {
+                    uint32_t& z = r[x >> 1][4 * j + 2 * (x & 1) + e];
+                    z = (see[j >> 2] >> (8 * (j & 3) + e)) & 1u ? z : 0xff800000u;
+                  }
+              }
             }
           };
           float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -1008,18 +974,17 @@ cudaError_t launch_shape(const PagedArgs& a, const TcMaps& maps, int ctas, cudaS
 cudaError_t launch_paged_tc(const PagedArgs& a, int ct, const dt_kv_cache* cache, int tiles,
                             cudaStream_t s) {
   TcMaps maps = {};
-  if (ct == DT_BF16) {
-    const uint64_t slots = (uint64_t)cache->n_pages * cache->Hkv * cache->page_size;
-    const uint32_t box = std::min(cache->page_size, 128);
-    if (!paged_map(&maps.k, cache->d_k, 2, a.d, slots, box) ||
-        !paged_map(&maps.v, cache->d_v, 2, a.d, slots, box))
+  const int bytes = ct == DT_BF16 ? 2 : 1;
+  const uint64_t slots = (uint64_t)cache->n_pages * cache->Hkv * cache->page_size;
+  const uint32_t box = std::min(cache->page_size, bytes == 2 || tiles == 2 ? 128 : 64);
+  if (!paged_map(&maps.k, cache->d_k, bytes, a.d, slots, box) ||
+      !paged_map(&maps.v, cache->d_v, bytes, a.d, slots, box))
+    return cudaErrorInvalidValue;
+  if (a.kt && bytes == 2) {
+    const uint64_t cols = (uint64_t)cache->Hkv * a.d;
+    if (!paged_map(&maps.kt, a.kt, 2, cols, a.total_rows, a.Nmax + 1) ||
+        !paged_map(&maps.vt, a.vt, 2, cols, a.total_rows, a.Nmax + 1))
       return cudaErrorInvalidValue;
-    if (a.kt) {
-      const uint64_t cols = (uint64_t)cache->Hkv * a.d;
-      if (!paged_map(&maps.kt, a.kt, 2, cols, a.total_rows, a.Nmax + 1) ||
-          !paged_map(&maps.vt, a.vt, 2, cols, a.total_rows, a.Nmax + 1))
-        return cudaErrorInvalidValue;
-    }
   }
   const int sms = std::min(dt_num_sms(), kPagedSms), ctas = tiles == 2 ? sms : 2 * sms;
 #define DT_PAGED(DD, CC)                                               \
