@@ -92,28 +92,23 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(taddr)
       : "memory");
 }
-// 16 rows x 64 columns, the layout of an mma.sync fragment: lane 4 i + j holds
+// 16 rows x 32 columns, the layout of an mma.sync fragment: lane 4 i + j holds
 // columns 8 k + 2 j, 8 k + 2 j + 1 of row i in r[4 k], r[4 k + 1] and of row
 // i + 8 in r[4 k + 2], r[4 k + 3].
-__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
 // The same fragment as pairs of 16-bit values: r[2 k] row i, r[2 k + 1] row i + 8.
-__device__ __forceinline__ void tmem_st_frag16(uint32_t taddr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_st_frag16(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-      "%13,%14,%15};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(taddr)
+      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
@@ -773,40 +768,41 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
             smask[q * 128 + row] = make_uint4(w[0], w[1], w[2], w[3]);
             __syncwarp();
           }
-          uint32_t r[2][32];  // 64 columns of rows lane / 4 + 0, 8 and + 16, 24
-          // scores of half hh: times the keys' scales, -infinity where the row does not see
-          auto load = [&](int hh) {
-            tmem_ld_frag(ts + 64 * hh, r[0]);
-            tmem_ld_frag(ts + (16u << 16) + 64 * hh, r[1]);
+          uint32_t r[2][16];  // 32 columns of rows lane / 4 + 0, 8 and + 16, 24
+          // scores of part c: times the keys' scales, -infinity where the row does not see
+          auto load = [&](int c) {
+            tmem_ld_frag(ts + 32 * c, r[0]);
+            tmem_ld_frag(ts + (16u << 16) + 32 * c, r[1]);
+            float2 f[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = *(const float2*)(kscale + 32 * c + 8 * j);
             tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float2 f = *(const float2*)(kscale + 64 * hh + 8 * j);
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
               for (int x = 0; x < 4; ++x)
-                mul2(r[x >> 1][4 * j + 2 * (x & 1)], r[x >> 1][4 * j + 2 * (x & 1) + 1], f.x, f.y);
-            }
+                mul2(r[x >> 1][4 * j + 2 * (x & 1)], r[x >> 1][4 * j + 2 * (x & 1) + 1], f[j].x,
+                     f[j].y);
             if (masked) {
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
-                const uint2 two = ((const uint2*)(rows + 8 * x))[hh];
-                const uint32_t see[2] = {two.x >> (2 * (lane & 3)), two.y >> (2 * (lane & 3))};
+                const uint32_t see = ((const uint32_t*)(rows + 8 * x))[c] >> (2 * (lane & 3));
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
+                for (int j = 0; j < 4; ++j)
 #pragma unroll
                   for (int e = 0; e < 2; ++e) {
                     uint32_t& z = r[x >> 1][4 * j + 2 * (x & 1) + e];
-                    z = (see[j >> 2] >> (8 * (j & 3) + e)) & 1u ? z : 0xff800000u;
+                    z = (see >> (8 * j + e)) & 1u ? z : 0xff800000u;
                   }
               }
             }
           };
           float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int c = 0; c < KT / 32; ++c) {
+            load(c);
 #pragma unroll
-          for (int hh = KT / 64 - 1; hh >= 0; --hh) {
-            load(hh);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
               for (int x = 0; x < 4; ++x)
                 top[x] = fmaxf(fmaxf(top[x], __uint_as_float(r[x >> 1][4 * j + 2 * (x & 1)])),
@@ -838,15 +834,17 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
           float less[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) less[x] = m4[x] == -INFINITY ? 0.f : -m4[x];
+#pragma unroll 1
+          for (int c = 0; c < KT / 32; ++c) {
+            load(c);
+            float2 f[4];
 #pragma unroll
-          for (int hh = 0; hh < KT / 64; ++hh) {
-            if (hh) load(hh);
+            for (int j = 0; j < 4; ++j) f[j] = *(const float2*)(kscale + KT + 32 * c + 8 * j);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-              uint32_t pk[16];
+              uint32_t pk[8];
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float2 f = *(const float2*)(kscale + KT + 64 * hh + 8 * j);
+              for (int j = 0; j < 4; ++j) {
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
                   const int x = 2 * t + z;
@@ -856,11 +854,11 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
                   p1 = ex2(p1);
                   l4[x] += p0 + p1;
                   uint32_t w0 = __float_as_uint(p0), w1 = __float_as_uint(p1);
-                  mul2(w0, w1, f.x, f.y);
+                  mul2(w0, w1, f[j].x, f[j].y);
                   pk[2 * j + z] = pack2(__uint_as_float(w0), __uint_as_float(w1));
                 }
               }
-              tmem_st_frag16(ts + (t ? 16u << 16 : 0u) + 32 * hh, pk);
+              tmem_st_frag16(ts + (t ? 16u << 16 : 0u) + 16 * c, pk);
             }
           }
         }
