@@ -273,45 +273,62 @@ def tree_build_sharded(cfg, rank, block_logits, markov_a, markov_b_shard, root_t
 
 
 # -------------------------------------------------------- paged KV cache --
-def _dense(where, device, **tensors):
-    """Each named tensor (None passes) is contiguous and on ``device``."""
-    for name, t in tensors.items():
-        if t is not None and (t.device != device or not t.is_contiguous()):
-            raise ValueError(f"{where}: {name} must be contiguous and on {device}")
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+_FLOATS = {torch.float32: _lib.DT_F32, torch.bfloat16: _lib.DT_BF16}
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _int32(where, device, **tensors):
-    _dense(where, device, **tensors)
-    for name, t in tensors.items():
-        if t is not None and t.dtype != torch.int32:
-            raise TypeError(f"{where}: {name} must be int32")
-
-
-def _shape(where, name, t, *shape):
-    if t is not None and tuple(t.shape) != shape:
+def _arg(where, name, t, dev, dtype, *shape):
+    """Address of a contiguous tensor of this device, type and shape.  (A serving step makes
+    several of these calls back to back: the checks are few and cheap.)"""
+    if t.dtype is not dtype:
+        raise TypeError(f"{where}: {name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
         raise ValueError(f"{where}: {name} must have shape {shape}, not {tuple(t.shape)}")
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be contiguous and on the device of the others")
+    return t.data_ptr()
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
+def _opt(where, name, t, dev, dtype, *shape):
+    return None if t is None else _arg(where, name, t, dev, dtype, *shape)
 
 
-def _run(fn, where, device, stream, *args):
-    """Call ``fn`` with ``device`` current and the stream as its last argument."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _run(fn, where, device, stream, *args)
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    check(fn(*args, s.cuda_stream), where)
+def _float_code(where, name, t):
+    code = _FLOATS.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{where}: {name} must be float32 or bfloat16, not {t.dtype}")
+    return code
 
 
-def _row_stride(where, name, t, heads, d):
+def _workspace(where, ws, dev):
+    if ws.get_device() != dev or ws.dtype is not torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"{where}: ws must be a contiguous uint8 tensor on the others' device")
+    return ws.data_ptr(), ws.numel()
+
+
+def _run(fn, where, dev, stream, *args):
+    """Call ``fn`` with device ``dev`` current and the stream as its last argument."""
+    if dev < 0:
+        raise ValueError(f"{where}: the tensors must be on a CUDA device")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _run(fn, where, dev, stream, *args)
+    code = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if code:
+        check(code, where)
+
+
+def _row_stride(where, name, t, dev, heads, d):
     """Elements between the rows of a [rows, heads, d] tensor whose rows are whole."""
     if t.dim() != 3 or t.shape[1:] != (heads, d):
         raise ValueError(f"{where}: {name} must have shape (rows, {heads}, {d})")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+    ld, head, one = t.stride()
+    if one != 1 or (heads > 1 and head != d):
         raise ValueError(f"{where}: the heads of a row of {name} must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * d)
+    if t.get_device() != dev:
+        raise ValueError(f"{where}: {name} must be on the device of the others")
+    return ld if t.shape[0] > 1 else max(ld, heads * d)
 
 
 class KVCache:
@@ -324,19 +341,17 @@ class KVCache:
         code = _lib.cache_dtype_code(k)
         if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype:
             raise ValueError("KVCache: k and v must be [n_pages, Hkv, page_size, d] of one type")
-        _dense("KVCache", k.device, k=k, v=v, k_scale=k_scale, v_scale=v_scale)
+        self.device = dev = k.get_device()
         scaled = code in (_lib.DT_E4M3, _lib.DT_I8)
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             if scaled != (t is not None):
                 raise ValueError(f"KVCache: {name} goes with the 8-bit types, and only with them")
-            if t is not None:
-                _shape("KVCache", name, t, *k.shape[:3])
-                if t.dtype != torch.float32:
-                    raise TypeError(f"KVCache: {name} must be float32")
+        at = [_arg("KVCache", name, t, dev, k.dtype, *k.shape) for name, t in (("k", k), ("v", v))]
+        at += [_opt("KVCache", name, t, dev, _F32, *k.shape[:3])
+               for name, t in (("k_scale", k_scale), ("v_scale", v_scale))]
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_pages, self.Hkv, self.page_size, self.d = k.shape
-        self._c = _lib.KvCacheStruct(_at(k), _at(v), _at(k_scale), _at(v_scale), self.n_pages,
-                                     self.page_size, self.Hkv, self.d, code)
+        self._c = _lib.KvCacheStruct(*at, self.n_pages, self.page_size, self.Hkv, self.d, code)
         self._ref = ctypes.byref(self._c)
 
     @staticmethod
@@ -348,12 +363,12 @@ class KVCache:
         return KVCache(new(), new(), scale(), scale())
 
 
-def _paged(where, cache, page_table, **per_request):
-    """Checks what every call on a cache takes; the batch size."""
-    _int32(where, cache.k.device, page_table=page_table, **per_request)
-    if page_table.dim() != 2:
+def _table(where, cache, t):
+    """Address and shape of a page table."""
+    if t.dim() != 2:
         raise ValueError(f"{where}: page_table must be [batch, max_pages]")
-    return page_table.shape[0]
+    batch, pages = t.shape
+    return _arg(where, "page_table", t, cache.device, _I32, batch, pages), batch, pages
 
 
 def kv_workspace_bytes() -> int:
@@ -363,58 +378,52 @@ def kv_workspace_bytes() -> int:
 def kv_write(k, v, row_start, pos, cache, page_table, ws, stream=None):
     """dt_kv_write: rows row_start[b] + i of k/v [rows, Hkv, d] (fp32 or bf16, any row stride) to
     positions pos[b] + i of request b; returns ``cache``."""
-    batch = _paged("kv_write", cache, page_table, row_start=row_start, pos=pos)
-    _shape("kv_write", "row_start", row_start, batch + 1)
-    _shape("kv_write", "pos", pos, batch)
-    if v.shape != k.shape or v.dtype != k.dtype or {k.device, v.device} != {cache.k.device}:
-        raise ValueError("kv_write: k and v must match and be on the cache's device")
-    if k.shape[0] == 0:
-        return cache
-    ld_k = _row_stride("kv_write", "k", k, cache.Hkv, cache.d)
-    ld_v = _row_stride("kv_write", "v", v, cache.Hkv, cache.d)
-    _run(_lib.lib.dt_kv_write, "dt_kv_write", k.device, stream, k.data_ptr(), v.data_ptr(), ld_k,
-         ld_v, dtype_code(k), row_start.data_ptr(), pos.data_ptr(), page_table.data_ptr(),
-         page_table.shape[1], batch, k.shape[0], cache._ref, ws.data_ptr(), ws.numel())
+    where, dev = "kv_write", cache.device
+    table, batch, pages = _table(where, cache, page_table)
+    starts = _arg(where, "row_start", row_start, dev, _I32, batch + 1)
+    first = _arg(where, "pos", pos, dev, _I32, batch)
+    if v.shape != k.shape or v.dtype is not k.dtype:
+        raise ValueError("kv_write: k and v must have one shape and type")
+    ld_k = _row_stride(where, "k", k, dev, cache.Hkv, cache.d)
+    ld_v = _row_stride(where, "v", v, dev, cache.Hkv, cache.d)
+    rows = k.shape[0]
+    if rows:
+        _run(_lib.lib.dt_kv_write, where, dev, stream, k.data_ptr(), v.data_ptr(), ld_k, ld_v,
+             _float_code(where, "k", k), starts, first, table, pages, batch, rows, cache._ref,
+             *_workspace(where, ws, dev))
     return cache
 
 
 def kv_commit(k_tree, v_tree, acc_nodes, n_acc, pos, cache, page_table, ws, stream=None):
     """dt_kv_commit: the root's and the accepted nodes' rows of k/v_tree [batch, Nmax+1, Hkv, d]
     to positions pos[b], pos[b] + 1, ...; returns ``cache``."""
-    batch = _paged("kv_commit", cache, page_table, acc_nodes=acc_nodes, n_acc=n_acc, pos=pos)
-    _dense("kv_commit", cache.k.device, k_tree=k_tree, v_tree=v_tree)
-    n1, Bk = k_tree.shape[1], acc_nodes.shape[1]
-    for name, t in (("k_tree", k_tree), ("v_tree", v_tree)):
-        _shape("kv_commit", name, t, batch, n1, cache.Hkv, cache.d)
-    if v_tree.dtype != k_tree.dtype:
-        raise TypeError("kv_commit: k_tree and v_tree must have one type")
-    _shape("kv_commit", "acc_nodes", acc_nodes, batch, Bk)
-    _shape("kv_commit", "n_acc", n_acc, batch)
-    _shape("kv_commit", "pos", pos, batch)
-    _run(_lib.lib.dt_kv_commit, "dt_kv_commit", k_tree.device, stream, k_tree.data_ptr(),
-         v_tree.data_ptr(), dtype_code(k_tree), acc_nodes.data_ptr(), n_acc.data_ptr(), Bk, n1 - 1,
-         pos.data_ptr(), page_table.data_ptr(), page_table.shape[1], batch, cache._ref,
-         ws.data_ptr(), ws.numel())
+    where, dev = "kv_commit", cache.device
+    table, batch, pages = _table(where, cache, page_table)
+    n1, Bk, dtype = k_tree.shape[1], acc_nodes.shape[1], k_tree.dtype
+    shape = batch, n1, cache.Hkv, cache.d
+    _run(_lib.lib.dt_kv_commit, where, dev, stream, _arg(where, "k_tree", k_tree, dev, dtype, *shape),
+         _arg(where, "v_tree", v_tree, dev, dtype, *shape), _float_code(where, "k_tree", k_tree),
+         _arg(where, "acc_nodes", acc_nodes, dev, _I32, batch, Bk),
+         _arg(where, "n_acc", n_acc, dev, _I32, batch), Bk, n1 - 1,
+         _arg(where, "pos", pos, dev, _I32, batch), table, pages, batch, cache._ref,
+         *_workspace(where, ws, dev))
     return cache
 
 
 def kv_read(cache, page_table, row_start, pos, k_out, v_out, ws, stream=None):
     """dt_kv_read: positions pos[b] + i into rows row_start[b] + i of k/v_out [rows, Hkv, d], the
     packed prefix that tree_verify_attn takes (prefix_start = row_start)."""
-    batch = _paged("kv_read", cache, page_table, row_start=row_start, pos=pos)
-    _dense("kv_read", cache.k.device, k_out=k_out, v_out=v_out)
-    _shape("kv_read", "row_start", row_start, batch + 1)
-    _shape("kv_read", "pos", pos, batch)
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        _shape("kv_read", name, t, k_out.shape[0], cache.Hkv, cache.d)
-    if v_out.dtype != k_out.dtype:
-        raise TypeError("kv_read: k_out and v_out must have one type")
-    if k_out.shape[0] == 0:
-        return k_out, v_out
-    _run(_lib.lib.dt_kv_read, "dt_kv_read", cache.k.device, stream, cache._ref,
-         page_table.data_ptr(), page_table.shape[1], row_start.data_ptr(), pos.data_ptr(), batch,
-         k_out.shape[0], dtype_code(k_out), k_out.data_ptr(), v_out.data_ptr(), ws.data_ptr(),
-         ws.numel())
+    where, dev, dtype = "kv_read", cache.device, k_out.dtype
+    table, batch, pages = _table(where, cache, page_table)
+    rows = k_out.shape[0]
+    shape = rows, cache.Hkv, cache.d
+    starts = _arg(where, "row_start", row_start, dev, _I32, batch + 1)
+    first = _arg(where, "pos", pos, dev, _I32, batch)
+    to_k = _arg(where, "k_out", k_out, dev, dtype, *shape)
+    to_v = _arg(where, "v_out", v_out, dev, dtype, *shape)
+    if rows:
+        _run(_lib.lib.dt_kv_read, where, dev, stream, cache._ref, table, pages, starts, first, batch,
+             rows, _float_code(where, "k_out", k_out), to_k, to_v, *_workspace(where, ws, dev))
     return k_out, v_out
 
 
@@ -427,20 +436,19 @@ def paged_attn(q, row_start, cache, page_table, kv_len, scale, out, ws, *, max_r
     """dt_paged_attn: causal attention of the chunk rows q [rows, Hq, d] (row_start[b] ..
     row_start[b+1] are request b's last tokens) over kv_len[b] cached positions.  window 0 = none;
     with one, the first n_sink positions stay visible.  No request has more than max_rows rows."""
-    batch = _paged("paged_attn", cache, page_table, row_start=row_start, kv_len=kv_len)
-    _shape("paged_attn", "row_start", row_start, batch + 1)
-    _shape("paged_attn", "kv_len", kv_len, batch)
-    _dense("paged_attn", cache.k.device, out=out)
-    if q.device != out.device or q.dtype != out.dtype or q.shape != out.shape or q.dim() != 3:
-        raise ValueError("paged_attn: q and out must be [rows, Hq, d], of one type and device")
+    where, dev = "paged_attn", cache.device
+    table, batch, pages = _table(where, cache, page_table)
+    starts = _arg(where, "row_start", row_start, dev, _I32, batch + 1)
+    lens = _arg(where, "kv_len", kv_len, dev, _I32, batch)
+    if q.dim() != 3:
+        raise ValueError("paged_attn: q must be [rows, Hq, d]")
     total, Hq, _ = q.shape
-    if total == 0:
-        return out
-    ld = _row_stride("paged_attn", "q", q, Hq, cache.d)
-    _run(_lib.lib.dt_paged_attn, "dt_paged_attn", q.device, stream, q.data_ptr(), ld,
-         row_start.data_ptr(), cache._ref, page_table.data_ptr(), page_table.shape[1],
-         kv_len.data_ptr(), batch, total, max_rows, Hq, scale, window, n_sink, dtype_code(q),
-         out.data_ptr(), ws.data_ptr(), ws.numel())
+    ld = _row_stride(where, "q", q, dev, Hq, cache.d)
+    to = _arg(where, "out", out, dev, q.dtype, total, Hq, cache.d)
+    if total:
+        _run(_lib.lib.dt_paged_attn, where, dev, stream, q.data_ptr(), ld, starts, cache._ref, table,
+             pages, lens, batch, total, max_rows, Hq, scale, window, n_sink,
+             _float_code(where, "q", q), to, *_workspace(where, ws, dev))
     return out
 
 
@@ -452,26 +460,20 @@ def tree_verify_attn_paged(q, cache, page_table, prefix_len, k_tree, v_tree, anc
                            out, ws, *, depths=None, window=0, n_sink=0, stream=None):
     """dt_tree_verify_attn_paged: tree_verify_attn over prefix_len[b] cached positions.  q/out
     [batch, Nmax+1, Hq, d]; k/v_tree [batch, Nmax+1, Hkv, d]; depths only with a window."""
-    where = "tree_verify_attn_paged"
-    batch = _paged(where, cache, page_table, prefix_len=prefix_len, n_nodes=n_nodes, depths=depths)
-    _dense(where, cache.k.device, q=q, k_tree=k_tree, v_tree=v_tree, anc=anc, out=out)
-    _, n1, Hq, _ = q.shape
-    for name, t, heads in (("q", q, Hq), ("out", out, Hq), ("k_tree", k_tree, cache.Hkv),
-                           ("v_tree", v_tree, cache.Hkv)):
-        _shape(where, name, t, batch, n1, heads, cache.d)
-        if t.dtype != q.dtype:
-            raise TypeError(f"{where}: {name} must have q's type")
-    if anc.dtype != torch.int64:
-        raise TypeError(f"{where}: anc must be int64")
-    _shape(where, "anc", anc, batch, n1 - 1)
-    _shape(where, "depths", depths, batch, n1 - 1)
-    _shape(where, "prefix_len", prefix_len, batch)
-    _shape(where, "n_nodes", n_nodes, batch)
-    _run(_lib.lib.dt_tree_verify_attn_paged, "dt_tree_verify_attn_paged", q.device, stream,
-         q.data_ptr(), cache._ref, page_table.data_ptr(), page_table.shape[1],
-         prefix_len.data_ptr(), k_tree.data_ptr(), v_tree.data_ptr(), anc.data_ptr(), _at(depths),
-         n_nodes.data_ptr(), batch, n1 - 1, Hq, scale, window, n_sink, dtype_code(q),
-         out.data_ptr(), ws.data_ptr(), ws.numel())
+    where, dev, dtype = "tree_verify_attn_paged", cache.device, q.dtype
+    table, batch, pages = _table(where, cache, page_table)
+    _, n1, Hq, d = q.shape
+    rows = batch, n1, cache.Hkv, cache.d
+    _run(_lib.lib.dt_tree_verify_attn_paged, where, dev, stream,
+         _arg(where, "q", q, dev, dtype, batch, n1, Hq, cache.d), cache._ref, table, pages,
+         _arg(where, "prefix_len", prefix_len, dev, _I32, batch),
+         _arg(where, "k_tree", k_tree, dev, dtype, *rows),
+         _arg(where, "v_tree", v_tree, dev, dtype, *rows),
+         _arg(where, "anc", anc, dev, _I64, batch, n1 - 1),
+         _opt(where, "depths", depths, dev, _I32, batch, n1 - 1),
+         _arg(where, "n_nodes", n_nodes, dev, _I32, batch), batch, n1 - 1, Hq, scale, window, n_sink,
+         _float_code(where, "q", q), _arg(where, "out", out, dev, dtype, batch, n1, Hq, cache.d),
+         *_workspace(where, ws, dev))
     return out
 
 
@@ -487,37 +489,8 @@ def logits_process(logits, out, ws, *, tokens=None, anc=None, n_nodes=None, hist
     """dt_logits_process: penalties, biases and masks on logits [batch, Nmax+1, V] (a tree's rows,
     with its tokens, anc and n_nodes) or [batch, 1, V] (no tree); ``out`` may be ``logits``.
     mask [rows, ceil(V / 32)] int32 words, one bit per allowed token."""
-    where, dev = "logits_process", logits.device
+    where, dev = "logits_process", logits.get_device()
     batch, n1, V = logits.shape
-    _dense(where, dev, logits=logits, out=out)
-    if out.shape != logits.shape or out.dtype != logits.dtype:
-        raise ValueError(f"{where}: out must have the shape and type of logits")
-    _int32(where, dev, tokens=tokens, n_nodes=n_nodes, history=history,
-           history_start=history_start, n_prompt=n_prompt, bias_start=bias_start,
-           bias_token=bias_token, mask=mask, mask_row=mask_row)
-    for name, t in (("repetition", repetition), ("presence", presence), ("frequency", frequency),
-                    ("bias_value", bias_value)):
-        if t is not None:
-            _dense(where, dev, **{name: t})
-            if t.dtype != torch.float32:
-                raise TypeError(f"{where}: {name} must be float32")
-            if name != "bias_value":
-                _shape(where, name, t, batch)
-    if anc is not None:
-        _dense(where, dev, anc=anc)
-        if anc.dtype != torch.int64:
-            raise TypeError(f"{where}: anc must be int64")
-    _shape(where, "tokens", tokens, batch, n1 - 1)
-    _shape(where, "anc", anc, batch, n1 - 1)
-    _shape(where, "n_nodes", n_nodes, batch)
-    _shape(where, "history_start", history_start, batch + 1)
-    _shape(where, "n_prompt", n_prompt, batch)
-    _shape(where, "bias_start", bias_start, batch + 1)
-    _shape(where, "mask_row", mask_row, batch, n1)
-    if bias_token is not None and bias_value is not None:
-        _shape(where, "bias_value", bias_value, bias_token.numel())
-    if mask is not None:
-        _shape(where, "mask", mask, mask.shape[0], (V + 31) // 32)
     # empty lists are no lists
     if history is not None and history.numel() == 0:
         history = history_start = n_prompt = None
@@ -526,11 +499,25 @@ def logits_process(logits, out, ws, *, tokens=None, anc=None, n_nodes=None, hist
     if mask is not None and mask.numel() == 0:
         mask = mask_row = None
     n = lambda t: 0 if t is None else t.shape[0]
-    _run(_lib.lib.dt_logits_process, "dt_logits_process", dev, stream, logits.data_ptr(),
-         dtype_code(logits), _at(tokens), _at(anc), _at(n_nodes), batch, n1 - 1, V, _at(history),
-         _at(history_start), _at(n_prompt), n(history), _at(repetition), _at(presence),
-         _at(frequency), _at(bias_start), _at(bias_token), _at(bias_value), n(bias_token),
-         _at(mask), _at(mask_row), n(mask), out.data_ptr(), ws.data_ptr(), ws.numel())
+    n_hist, n_bias, n_mask = n(history), n(bias_token), n(mask)
+    _run(_lib.lib.dt_logits_process, where, dev, stream,
+         _arg(where, "logits", logits, dev, logits.dtype, batch, n1, V),
+         _float_code(where, "logits", logits),
+         _opt(where, "tokens", tokens, dev, _I32, batch, n1 - 1),
+         _opt(where, "anc", anc, dev, _I64, batch, n1 - 1),
+         _opt(where, "n_nodes", n_nodes, dev, _I32, batch), batch, n1 - 1, V,
+         _opt(where, "history", history, dev, _I32, n_hist),
+         _opt(where, "history_start", history_start, dev, _I32, batch + 1),
+         _opt(where, "n_prompt", n_prompt, dev, _I32, batch), n_hist,
+         _opt(where, "repetition", repetition, dev, _F32, batch),
+         _opt(where, "presence", presence, dev, _F32, batch),
+         _opt(where, "frequency", frequency, dev, _F32, batch),
+         _opt(where, "bias_start", bias_start, dev, _I32, batch + 1),
+         _opt(where, "bias_token", bias_token, dev, _I32, n_bias),
+         _opt(where, "bias_value", bias_value, dev, _F32, n_bias), n_bias,
+         _opt(where, "mask", mask, dev, _I32, n_mask, (V + 31) // 32),
+         _opt(where, "mask_row", mask_row, dev, _I32, batch, n1), n_mask,
+         _arg(where, "out", out, dev, logits.dtype, batch, n1, V), *_workspace(where, ws, dev))
     return out
 
 

@@ -7,44 +7,67 @@
 // rounding moves a code only where x * X / a is within 2^-24 of a border.
 // 2^-100 keeps X / a finite.  Read: code * scale, rounded once.
 //
-// Both only move data: a thread owns 8 consecutive values of a head row (one
-// 16-byte piece of bf16) of K and of V, d / 8 neighbouring lanes own a row and
-// find its largest magnitude with shuffles.
+// Both only move data, and what bounds them is memory bandwidth: a warp takes
+// a token, looks its request and slot up once, and asks for up to kUnroll pieces
+// of 8 values a lane of K and of V before it works on the first.  d / 8
+// neighbouring lanes own a head row and find its largest magnitude with shuffles.
 #include "kv_cache.cuh"
 
 namespace dt {
 namespace {
 
 constexpr int kKvThreads = 256;
-constexpr int kPer = 8;  // values per thread
+constexpr int kPer = 8;     // values of a piece
+constexpr int kUnroll = 4;  // pieces of K, and of V, that a lane has on their way
 
-// 8 values at p (elements of type DT), as fp32; VEC: p is 16-byte aligned
+// A piece as it lies in memory, 8 values of type DT; VEC: 16-byte aligned.
+// (Pieces wait in this form: turned into fp32 at once they would take twice the
+// registers, and half the warps would fit.)
+template <int DT>
+struct Piece {
+  static constexpr int W = DT == DT_F32 ? 8 : DT == DT_BF16 ? 4 : 2;
+  uint32_t w[W];
+};
 template <int DT, bool VEC>
-__device__ __forceinline__ void load8(const void* base, int64_t off, float (&x)[kPer]) {
+__device__ __forceinline__ Piece<DT> load8(const void* base, int64_t off) {
+  Piece<DT> r;
   if constexpr (DT == DT_F32) {
-    const float* p = (const float*)base + off;
-    if constexpr (VEC) {
-      const float4 a = ((const float4*)p)[0], b = ((const float4*)p)[1];
-      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-      x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
+    const uint32_t* p = (const uint32_t*)base + off;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) x[i] = p[i];
+    for (int i = 0; i < 8; i += 4) {
+      if constexpr (VEC) {
+        const uint4 x = *(const uint4*)(p + i);
+        r.w[i] = x.x, r.w[i + 1] = x.y, r.w[i + 2] = x.z, r.w[i + 3] = x.w;
+      } else {
+#pragma unroll
+        for (int e = i; e < i + 4; ++e) r.w[e] = p[e];
+      }
     }
-  } else {
+  } else if constexpr (DT == DT_BF16) {
     const uint16_t* p = (const uint16_t*)base + off;
     if constexpr (VEC) {
-      const uint4 a = *(const uint4*)p;
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
+      const uint4 x = *(const uint4*)p;
+      r.w[0] = x.x, r.w[1] = x.y, r.w[2] = x.z, r.w[3] = x.w;
     } else {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) x[i] = bf16_to_f32(p[i]);
+      for (int i = 0; i < 4; ++i) r.w[i] = p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
     }
+  } else {
+    const uint2 x = *(const uint2*)((const uint8_t*)base + off);
+    r.w[0] = x.x, r.w[1] = x.y;
+  }
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ void values8(const Piece<DT>& r, float scale, float (&x)[kPer]) {
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if constexpr (DT == DT_F32)
+      x[i] = __uint_as_float(r.w[i]);
+    else if constexpr (DT == DT_BF16)
+      x[i] = __uint_as_float(i & 1 ? r.w[i / 2] & 0xffff0000u : r.w[i / 2] << 16);
+    else
+      x[i] = Code<DT>::get((typename Code<DT>::T)((r.w[i / 4] >> (8 * (i & 3))) & 0xff)) * scale;
   }
 }
 
@@ -122,56 +145,62 @@ struct WriteArgs {
   int32_t* status;
 };
 
-// grid: total_rows * Hkv * d / 8 threads (commit: batch * (Bk + 1) rows)
+// a warp per row (commit: batch * (Bk + 1) rows)
 template <int ST, int CT, bool VEC, bool COMMIT>
 __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(WriteArgs a) {
-  const int pieces = a.d / kPer;
-  const int64_t t = (int64_t)blockIdx.x * kKvThreads + threadIdx.x;
-  const int64_t hr = t / pieces;  // head row: (row, head)
-  const int at = (int)(t % pieces) * kPer;
-  const int h = (int)(hr % a.c.Hkv);
-  const int64_t r = hr / a.c.Hkv;
-  int64_t slot = -1, src = 0;
+  const int lane = threadIdx.x & 31, d = a.d, shift = d == 128 ? 7 : 6;
+  const int r = blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5);
+  int b = -1;
+  int64_t src = 0, p = 0;
   if (COMMIT) {
-    const int b = (int)(r / (a.Bk + 1)), i = (int)(r % (a.Bk + 1));
-    if (b < a.batch) {
-      const int n = a.n_acc[b];
-      if (n < 0 || n > a.Bk) set_status(a.status, DT_EDEVICE);
-      if (i <= min(n, a.Bk)) {
-        const int node = i ? a.acc[(int64_t)b * a.Bk + i - 1] : -1;
-        const int64_t p = (int64_t)a.pos[b] + i;
-        if (n < 0 || node < -1 || node >= a.Nmax || (i && node < 0) || p < 0 || p >= 1ll << 31)
-          set_status(a.status, DT_EDEVICE);
-        else {
-          src = (int64_t)b * (a.Nmax + 1) + node + 1;
-          slot = a.c.slot(b, (int)p, a.status);
-        }
-      }
+    b = r / (a.Bk + 1);
+    const int i = r % (a.Bk + 1);
+    if (b >= a.batch) return;
+    const int n = a.n_acc[b];
+    if (n < 0 || n > a.Bk) set_status(a.status, DT_EDEVICE);
+    if (n < 0 || i > min(n, a.Bk)) return;
+    const int node = i ? a.acc[(int64_t)b * a.Bk + i - 1] : -1;
+    if (node < -1 || node >= a.Nmax || (i && node < 0)) {
+      set_status(a.status, DT_EDEVICE);
+      return;
     }
-  } else if (r < a.total_rows) {
-    const int b = row_request(a.row_start, a.batch, (int)r);
-    if (b >= 0) {
-      const int64_t p = (int64_t)a.pos[b] + ((int)r - a.row_start[b]);
-      if (p < 0 || p >= 1ll << 31)
-        set_status(a.status, DT_EDEVICE);
-      else {
-        src = r;
-        slot = a.c.slot(b, (int)p, a.status);
-      }
-    }
-  }
-  float k[kPer], v[kPer];
-  const int64_t in = (int64_t)h * a.d + at;
-  if (slot >= 0) {
-    load8<ST, VEC>(a.k, src * a.ld_k + in, k);
-    load8<ST, VEC>(a.v, src * a.ld_v + in, v);
-    slot += (int64_t)h << a.c.page_shift;
+    src = (int64_t)b * (a.Nmax + 1) + node + 1;
+    p = (int64_t)a.pos[b] + i;
   } else {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) k[i] = v[i] = 0.f;
+    if (r >= a.total_rows) return;
+    b = row_request_warp(a.row_start, a.pos, a.batch, r, p);
+    if (b < 0) return;
+    src = r;
   }
-  put8<CT>(a.c.k, a.c.ks, slot, a.d, at, k);
-  put8<CT>(a.c.v, a.c.vs, slot, a.d, at, v);
+  if (p < 0 || p >= 1ll << 31) {
+    set_status(a.status, DT_EDEVICE);
+    return;
+  }
+  const int64_t slot = a.c.slot(b, (int)p, a.status);
+  if (slot < 0) return;
+  const int all = a.c.Hkv * d / kPer;
+  for (int x0 = lane; x0 - lane < all; x0 += 32 * kUnroll) {  // (whole warps: put8 shuffles)
+    Piece<ST> k[kUnroll] = {}, v[kUnroll] = {};
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int x = x0 + 32 * u;
+      if (x < all) {
+        k[u] = load8<ST, VEC>(a.k, src * a.ld_k + x * kPer);
+        v[u] = load8<ST, VEC>(a.v, src * a.ld_v + x * kPer);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int x = x0 + 32 * u, h = x * kPer >> shift, at = (x * kPer) & (d - 1);
+      if (x - lane >= all) break;
+      const int64_t to = x < all ? slot + ((int64_t)h << a.c.page_shift) : -1;
+      float y[kPer];
+      values8<ST>(k[u], 1.f, y);
+      put8<CT>(a.c.k, a.c.ks, to, d, at, y);
+      values8<ST>(v[u], 1.f, y);
+      put8<CT>(a.c.v, a.c.vs, to, d, at, y);
+    }
+  }
 }
 
 struct ReadArgs {
@@ -184,57 +213,54 @@ struct ReadArgs {
   int32_t* status;
 };
 
-template <int CT>
-__device__ __forceinline__ void get8(const void* cache, const float* scales, int64_t slot, int d,
-                                     int at, float (&x)[kPer]) {
-  if constexpr (CT == DT_F32 || CT == DT_BF16) {
-    load8<CT, true>(cache, slot * d + at, x);
-  } else {
-    const uint2 w = *(const uint2*)((const uint8_t*)cache + slot * d + at);
-    const float s = scales[slot];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const uint32_t byte = ((i < 4 ? w.x : w.y) >> (8 * (i & 3))) & 0xff;
-      x[i] = Code<CT>::get((typename Code<CT>::T)byte) * s;
-    }
-  }
-}
-
 template <int CT, int OT>
 __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(ReadArgs a) {
-  const int pieces = a.d / kPer;
-  const int64_t t = (int64_t)blockIdx.x * kKvThreads + threadIdx.x;
-  const int64_t hr = t / pieces;
-  const int at = (int)(t % pieces) * kPer;
-  const int h = (int)(hr % a.c.Hkv);
-  const int64_t r = hr / a.c.Hkv;
+  const int lane = threadIdx.x & 31, d = a.d, shift = d == 128 ? 7 : 6;
+  const int r = blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5);
   if (r >= a.total_rows) return;
-  const int b = row_request(a.row_start, a.batch, (int)r);
+  int64_t p = 0, slot = -1;
+  const int b = row_request_warp(a.row_start, a.pos, a.batch, r, p);
   if (b < 0) return;
-  const int64_t p = (int64_t)a.pos[b] + ((int)r - a.row_start[b]);
-  int64_t slot = -1;
   if (p < 0 || p >= 1ll << 31)
     set_status(a.status, DT_EDEVICE);
   else
     slot = a.c.slot(b, (int)p, a.status);
-  float k[kPer], v[kPer];
-  if (slot >= 0) {
-    slot += (int64_t)h << a.c.page_shift;
-    get8<CT>(a.c.k, a.c.ks, slot, a.d, at, k);
-    get8<CT>(a.c.v, a.c.vs, slot, a.d, at, v);
-  } else {
+  const int all = a.c.Hkv * d / kPer;
+  const int64_t out = (int64_t)r * a.c.Hkv * d;
+  constexpr bool kScaled = CT == DT_E4M3 || CT == DT_I8;
+  for (int x0 = lane; x0 < all; x0 += 32 * kUnroll) {
+    Piece<CT> k[kUnroll] = {}, v[kUnroll] = {};
+    float ks[kUnroll], vs[kUnroll];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) k[i] = v[i] = 0.f;
+    for (int u = 0; u < kUnroll; ++u) {
+      const int x = x0 + 32 * u, h = x * kPer >> shift, at = (x * kPer) & (d - 1);
+      ks[u] = vs[u] = 0.f;
+      if (x < all && slot >= 0) {
+        const int64_t from = slot + ((int64_t)h << a.c.page_shift);
+        k[u] = load8<CT, true>(a.c.k, from * d + at);
+        v[u] = load8<CT, true>(a.c.v, from * d + at);
+        if constexpr (kScaled) {
+          ks[u] = a.c.ks[from];
+          vs[u] = a.c.vs[from];
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int x = x0 + 32 * u;
+      if (x >= all) break;
+      float y[kPer];
+      values8<CT>(k[u], ks[u], y);
+      store8<OT>(a.k_out, out + x * kPer, y);
+      values8<CT>(v[u], vs[u], y);
+      store8<OT>(a.v_out, out + x * kPer, y);
+    }
   }
-  const int64_t out = hr * a.d + at;
-  store8<OT>(a.k_out, out, k);
-  store8<OT>(a.v_out, out, v);
 }
 
 template <int ST, bool VEC, bool COMMIT>
 void launch_write(const WriteArgs& a, int ct, int64_t rows, cudaStream_t s) {
-  const int64_t threads = rows * a.c.Hkv * (a.d / kPer);
-  const unsigned grid = (unsigned)((threads + kKvThreads - 1) / kKvThreads);
+  const unsigned grid = (unsigned)((rows + kKvThreads / 32 - 1) / (kKvThreads / 32));
   switch (ct) {
     case DT_F32: kv_write_kernel<ST, DT_F32, VEC, COMMIT><<<grid, kKvThreads, 0, s>>>(a); break;
     case DT_BF16: kv_write_kernel<ST, DT_BF16, VEC, COMMIT><<<grid, kKvThreads, 0, s>>>(a); break;
@@ -245,8 +271,6 @@ void launch_write(const WriteArgs& a, int ct, int64_t rows, cudaStream_t s) {
 
 template <bool COMMIT>
 dt_status run_write(const WriteArgs& a, int st, int ct, int64_t rows, cudaStream_t s) {
-  const int64_t blocks = (rows * a.c.Hkv * (a.d / kPer) + kKvThreads - 1) / kKvThreads;
-  if (blocks >= 1ll << 31) return DT_EUNSUPPORTED;
   if (rows == 0) return DT_OK;
   // 16-byte loads where every row of every head starts on 16 bytes
   const int es = kv_code_bytes(st);
@@ -347,9 +371,7 @@ dt_status dt_kv_read(const dt_kv_cache* cache, const int32_t* d_page_table, int 
   if (dt != DT_F32 && dt != DT_BF16) return DT_EINVAL;
   if (((uintptr_t)d_k_out | (uintptr_t)d_v_out) & 15) return DT_EINVAL;
   if (!ws || ws_bytes < kWsHeader) return DT_EWORKSPACE;
-  const int64_t blocks =
-      ((int64_t)total_rows * cache->Hkv * (cache->d / kPer) + kKvThreads - 1) / kKvThreads;
-  if (blocks >= 1ll << 31) return DT_EUNSUPPORTED;
+  const int64_t blocks = ((int64_t)total_rows + kKvThreads / 32 - 1) / (kKvThreads / 32);
   if (total_rows == 0) return DT_OK;
   ReadArgs a;
   a.c = kv_view(cache, d_page_table, max_pages);

@@ -3,6 +3,7 @@
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
+#include <limits.h>
 
 #include "common.cuh"
 
@@ -81,6 +82,31 @@ __device__ __forceinline__ int row_request(const int32_t* start, int batch, int 
     else
       hi = mid;
   }
+  return lo;
+}
+
+// The same by a whole warp, and the row's position: pos[b] + r - start[b].  Up
+// to 31 requests take one look, in which the positions come along.
+__device__ __forceinline__ int row_request_warp(const int32_t* start, const int32_t* pos, int batch,
+                                                int r, int64_t& p) {
+  const int lane = threadIdx.x & 31;
+  if (batch < 32) {
+    const int s = lane <= batch ? start[lane] : INT_MAX, q = lane < batch ? pos[lane] : 0;
+    // the last start that is not behind r
+    const int b = __popc(__ballot_sync(0xffffffffu, s <= r)) - 1;
+    if (b < 0 || b >= batch) return -1;
+    p = (int64_t)__shfl_sync(0xffffffffu, q, b) + (r - __shfl_sync(0xffffffffu, s, b));
+    return b;
+  }
+  if (r < start[0] || r >= start[batch]) return -1;
+  int lo = 0, hi = batch;  // start[lo] <= r < start[hi]
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + (1 + lane) * step;
+    const int n = __popc(__ballot_sync(0xffffffffu, at < hi && start[min(at, hi)] <= r));
+    lo += n * step;
+    hi = min(lo + step, hi);
+  }
+  p = (int64_t)pos[lo] + (r - start[lo]);
   return lo;
 }
 

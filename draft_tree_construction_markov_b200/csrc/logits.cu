@@ -3,17 +3,22 @@
 // A CTA owns a slice of the vocabulary for one request and some of its rows.
 // It first counts the request's history into a shared-memory table of its
 // slice (one word per token: generated count, prompt flag), together with the
-// slice's bias entries and the tree nodes whose token falls in it, and marks
-// every token that any of these touch in a bitmap.  Then it streams the rows:
-// a thread takes 8 neighbouring tokens (one 16-byte load of bf16), one byte
-// of the bitmap and one byte of the row's mask.  Most groups are untouched and
-// are copied; a touched token's count is the table's plus the nodes of the list
-// that hold it and lie on the row's path (a bit of the row's ancestor word).
-// Groups the mask forbids whole are written without being read, and in place
-// an untouched, allowed group is neither read nor written.
+// slice's bias entries and the tree nodes whose token falls in it, and lists the
+// tokens that any of these touch.  Then it streams the rows with their masks, a
+// thread taking 8 neighbouring tokens (one 16-byte load of bf16), several rows
+// on their way at once; groups that the mask forbids whole are written without
+// being read, and in place a group without a forbidden token is not touched at
+// all.  At last the threads share the listed tokens of all rows out among
+// themselves and settle them one by one: common tokens are neighbours in the
+// vocabulary, and left to the threads that stream them they would make a few
+// threads of one slice do all of the work.  A token's count on a path is the
+// table's plus the bits that the row's ancestor word and the word of the nodes
+// that hold the token have in common.
 //
 // Bound: memory, each live row read and written once; the history is re-read
 // by every slice of its request, from L2.
+#include <limits.h>
+
 #include "common.cuh"
 
 namespace dt {
@@ -22,8 +27,9 @@ namespace {
 constexpr int kLgThreads = 256;
 constexpr int kLgSlice = 4096;                 // tokens per CTA
 constexpr int kLgTab = kLgSlice + 8;           // rows start up to 7 tokens into a group of 8
-constexpr int kLgWords = (kLgTab + 31) / 32 + 1;
 constexpr int kLgGroups = kLgSlice / 8 / kLgThreads;  // groups per thread and row
+template <bool BF16>
+constexpr int kLgRows = BF16 ? 4 : 2;                 // rows at a time
 
 struct LogitsArgs {
   const void* in;
@@ -74,9 +80,9 @@ __global__ void __launch_bounds__(kLgThreads) logits_kernel(LogitsArgs a) {
   constexpr int W = BF16 ? 4 : 8;  // 32-bit words of a group of 8 tokens
   __shared__ uint32_t cnt[kLgTab];
   __shared__ uint32_t bidx[kLgTab];
-  __shared__ uint32_t touched[kLgWords];
+  __shared__ uint16_t listed[kLgTab];            // table entries that something touches
   __shared__ int node_tok[64], node_id[64];
-  __shared__ int n_list;
+  __shared__ int n_nodes_here, n_listed;
   const int tid = threadIdx.x, b = blockIdx.y;
   const int base = blockIdx.x * kLgSlice - 8;  // token of table entry 0
   int n = 0;
@@ -91,21 +97,27 @@ __global__ void __launch_bounds__(kLgThreads) logits_kernel(LogitsArgs a) {
 
   // ---- the slice's table
   for (int i = tid; i < kLgTab; i += kLgThreads) cnt[i] = bidx[i] = 0;
-  if (tid == 0) n_list = 0;
-  if (tid < kLgWords) touched[tid] = 0;
+  if (tid == 0) n_nodes_here = n_listed = 0;
   __syncthreads();
   if (a.hist) {
     const int2 r = list_range(a.hist_start, b, a.n_hist, a.status);
     const int np = a.n_prompt ? min(max(a.n_prompt[b], 0), r.y - r.x) : 0;
-    for (int i = r.x + tid; i < r.y; i += kLgThreads) {
-      const int x = a.hist[i];
-      if (x < 0 || x >= a.V) {
-        set_status(a.status, DT_EDEVICE);
-      } else if ((uint32_t)(x - base) < (uint32_t)kLgTab) {
-        if (i - r.x < np)
-          atomicOr(&cnt[x - base], 0x80000000u);
-        else
-          atomicAdd(&cnt[x - base], 1u);
+    for (int i0 = r.x + tid; i0 < r.y; i0 += 4 * kLgThreads) {
+      int x4[4];  // (four loads on their way)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x4[k] = i0 + k * kLgThreads < r.y ? a.hist[i0 + k * kLgThreads] : 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = i0 + k * kLgThreads, x = x4[k];
+        if (i >= r.y) break;
+        if (x < 0 || x >= a.V) {
+          set_status(a.status, DT_EDEVICE);
+        } else if ((uint32_t)(x - base) < (uint32_t)kLgTab) {
+          if (i - r.x < np)
+            atomicOr(&cnt[x - base], 0x80000000u);
+          else
+            atomicAdd(&cnt[x - base], 1u);
+        }
       }
     }
   }
@@ -125,133 +137,158 @@ __global__ void __launch_bounds__(kLgThreads) logits_kernel(LogitsArgs a) {
     if (x < 0 || x >= a.V) {
       set_status(a.status, DT_EDEVICE);
     } else if ((uint32_t)(x - base) < (uint32_t)kLgTab) {
-      const int k = atomicAdd(&n_list, 1);
-      node_tok[k] = x;
+      const int k = atomicAdd(&n_nodes_here, 1);
+      node_tok[k] = x - base;
       node_id[k] = tid;
-      atomicOr(&touched[(x - base) >> 5], 1u << ((x - base) & 31));
+      atomicOr(&cnt[x - base], 0x40000000u);  // a node holds it
     }
   }
   __syncthreads();
-  for (int i = tid; i < (kLgWords - 1) * 32; i += kLgThreads) {
+  for (int i0 = 0; i0 < kLgTab; i0 += kLgThreads) {
+    const int i = i0 + tid;
     const bool t = i < kLgTab && (cnt[i] | bidx[i]);
     const uint32_t w = __ballot_sync(0xffffffffu, t);
-    if ((tid & 31) == 0 && w) atomicOr(&touched[i >> 5], w);
+    int at = 0;
+    if ((tid & 31) == 0 && w) at = atomicAdd(&n_listed, __popc(w));
+    at = __shfl_sync(0xffffffffu, at, 0);
+    // (their order does not matter: every token is settled by itself)
+    if (t) listed[at + __popc(w & ((1u << (tid & 31)) - 1))] = (uint16_t)i;
   }
   __syncthreads();
-  const int nl = n_list;
+  const int nl = n_nodes_here, n_touched = n_listed;
   const float rep = a.rep ? a.rep[b] : 1.f, pres = a.pres ? a.pres[b] : 0.f,
               freq = a.freq ? a.freq[b] : 0.f;
   const int nw = (a.V + 31) / 32;
 
   // ---- the rows
-  for (int i = blockIdx.z; i <= n; i += gridDim.z) {
-    const int64_t row = (int64_t)b * (a.Nmax + 1) + i;
-    const int64_t R = row * a.V;
-    const int off = (int)(R & 7);  // groups of 8 are aligned in memory
-    const uint64_t on = i ? a.anc[(int64_t)b * a.Nmax + i - 1] : 0ull;
-    const uint32_t* mask = nullptr;
-    if (a.mask) {
-      const int64_t m = a.mask_row ? a.mask_row[row] : row;
-      if (m < -1 || m >= a.n_mask_rows) {
-        if (tid == 0) set_status(a.status, DT_EDEVICE);
-      } else if (m >= 0) {
-        mask = a.mask + m * nw;
+  constexpr int RB = kLgRows<BF16>;
+  for (int i0 = blockIdx.z; i0 <= n; i0 += RB * gridDim.z) {
+    int64_t R[RB];            // first element of row k
+    const uint32_t* mask[RB];
+    int mrow[RB];
+#pragma unroll
+    for (int k = 0; k < RB; ++k) {
+      const int i = i0 + k * gridDim.z;
+      const int64_t row = (int64_t)b * (a.Nmax + 1) + i;
+      R[k] = row * a.V;
+      mrow[k] = -1;
+      if (a.mask && i <= n) mrow[k] = a.mask_row ? a.mask_row[row] : (int)min(row, (int64_t)INT_MAX);
+    }
+#pragma unroll
+    for (int k = 0; k < RB; ++k) {
+      mask[k] = nullptr;
+      if (mrow[k] < -1 || mrow[k] >= a.n_mask_rows) {
+        if (tid == 0 && (a.mask && i0 + k * (int)gridDim.z <= n)) set_status(a.status, DT_EDEVICE);
+      } else if (mrow[k] >= 0) {
+        mask[k] = a.mask + (int64_t)mrow[k] * nw;
       }
     }
-    // one touched token's value
-    auto settle = [&](float z, int x) {
-      const uint32_t c = cnt[x - base];
-      uint32_t made = c & 0x7fffffffu;
-      for (int k = 0; k < nl; ++k)
-        if (node_tok[k] == x && ((on >> node_id[k]) & 1ull)) ++made;
-      if (made || (c >> 31)) z = z > 0.f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
-      if (made) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, (float)made)), pres);
-      const uint32_t bi = bidx[x - base];
-      if (bi) z = __fadd_rn(z, a.bias_value[br.x + bi - 1]);
-      return z;
+    uint32_t u[RB][kLgGroups][W];
+    uint32_t mb[RB][kLgGroups];
+    auto first = [&](int k, int j) {  // first token of the thread's group j of row k
+      return (blockIdx.x * (kLgSlice / 8) + j * kLgThreads + tid) * 8 - (int)(R[k] & 7);
     };
-    uint32_t u[kLgGroups][W];
-    uint32_t tb[kLgGroups], mb[kLgGroups];
 #pragma unroll
-    for (int j = 0; j < kLgGroups; ++j) {
-      const int t0 = (blockIdx.x * (kLgSlice / 8) + j * kLgThreads + tid) * 8 - off;
-      const bool full = t0 >= 0 && t0 + 8 <= a.V;
-      tb[j] = bits8(touched, t0 - base, kLgWords);
-      mb[j] = 0xffu;
-      if (mask) mb[j] = bits8(mask, t0, nw);
-      const bool need = full && mb[j] != 0 && !(INPLACE && tb[j] == 0 && mb[j] == 0xffu);
-      if (need) {
-        const uint4* p = (const uint4*)((const uint8_t*)a.in + (R + t0) * (BF16 ? 2 : 4));
+    for (int k = 0; k < RB; ++k)
 #pragma unroll
-        for (int w = 0; w < W / 4; ++w) {
-          const uint4 q = p[w];
-          u[j][4 * w] = q.x, u[j][4 * w + 1] = q.y, u[j][4 * w + 2] = q.z, u[j][4 * w + 3] = q.w;
+      for (int j = 0; j < kLgGroups; ++j)
+        mb[k][j] = mask[k] ? bits8(mask[k], first(k, j), nw) : 0xffu;
+#pragma unroll
+    for (int k = 0; k < RB; ++k) {
+      const bool live = i0 + k * (int)gridDim.z <= n;
+#pragma unroll
+      for (int j = 0; j < kLgGroups; ++j) {
+        const int t0 = first(k, j);
+#pragma unroll
+        for (int w = 0; w < W; ++w) u[k][j][w] = 0;
+        if (live && t0 >= 0 && t0 + 8 <= a.V && mb[k][j] != 0 && !(INPLACE && mb[k][j] == 0xffu)) {
+          const uint4* p = (const uint4*)((const uint8_t*)a.in + (R[k] + t0) * (BF16 ? 2 : 4));
+#pragma unroll
+          for (int w = 0; w < W / 4; ++w) {
+            const uint4 q = p[w];
+            u[k][j][4 * w] = q.x, u[k][j][4 * w + 1] = q.y;
+            u[k][j][4 * w + 2] = q.z, u[k][j][4 * w + 3] = q.w;
+          }
         }
-      } else {
-#pragma unroll
-        for (int w = 0; w < W; ++w) u[j][w] = 0;
       }
     }
 #pragma unroll
-    for (int j = 0; j < kLgGroups; ++j) {
-      const int t0 = (blockIdx.x * (kLgSlice / 8) + j * kLgThreads + tid) * 8 - off;
-      if (t0 >= 0 && t0 + 8 <= a.V) {
-        if (INPLACE && tb[j] == 0 && mb[j] == 0xffu) continue;
-        uint32_t t = tb[j] & mb[j];
-        while (t) {
-          const int e = __ffs(t) - 1;
-          t &= t - 1;
-          const int wi = BF16 ? e >> 1 : e;
-          uint32_t word = 0;
+    for (int k = 0; k < RB; ++k) {
+      if (i0 + k * (int)gridDim.z > n) break;
 #pragma unroll
-          for (int w = 0; w < W; ++w)
-            if (w == wi) word = u[j][w];
-          if (BF16) {
-            const int sh = 16 * (e & 1);
-            const float z = settle(__uint_as_float((word >> sh) << 16), t0 + e);
-            uint32_t r;
-            asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(r) : "f"(z));
-            word = (word & (0xffff0000u >> sh)) | ((r & 0xffffu) << sh);
-          } else {
-            word = __float_as_uint(settle(__uint_as_float(word), t0 + e));
-          }
+      for (int j = 0; j < kLgGroups; ++j) {
+        const int t0 = first(k, j);
+        uint32_t(&v)[W] = u[k][j];
+        const uint32_t m = mb[k][j];
+        if (INPLACE && m == 0xffu) continue;
+        if (t0 >= 0 && t0 + 8 <= a.V) {
+          if (m != 0xffu) {
 #pragma unroll
-          for (int w = 0; w < W; ++w)
-            if (w == wi) u[j][w] = word;
-        }
-        if (mb[j] != 0xffu) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (BF16) {
-              if (!((mb[j] >> e) & 1u))
-                u[j][e >> 1] = (e & 1) ? (u[j][e >> 1] & 0x0000ffffu) | 0xff800000u
-                                       : (u[j][e >> 1] & 0xffff0000u) | 0x0000ff80u;
-            } else if (!((mb[j] >> e) & 1u)) {
-              u[j][e] = 0xff800000u;
+            for (int e = 0; e < 8; ++e) {
+              if (BF16) {
+                if (!((m >> e) & 1u))
+                  v[e >> 1] = (e & 1) ? (v[e >> 1] & 0x0000ffffu) | 0xff800000u
+                                      : (v[e >> 1] & 0xffff0000u) | 0x0000ff80u;
+              } else if (!((m >> e) & 1u)) {
+                v[e] = 0xff800000u;
+              }
             }
           }
-        }
-        uint4* p = (uint4*)((uint8_t*)a.out + (R + t0) * (BF16 ? 2 : 4));
+          uint4* p = (uint4*)((uint8_t*)a.out + (R[k] + t0) * (BF16 ? 2 : 4));
 #pragma unroll
-        for (int w = 0; w < W / 4; ++w)
-          p[w] = make_uint4(u[j][4 * w], u[j][4 * w + 1], u[j][4 * w + 2], u[j][4 * w + 3]);
-      } else if (t0 + 8 > 0 && t0 < a.V) {
-        // a group cut by the row's start or end: token by token
-        for (int e = 0; e < 8; ++e) {
-          const int x = t0 + e;
-          if (x < 0 || x >= a.V) continue;
-          const int64_t at = R + x;
-          float z = BF16 ? bf16_to_f32(((const uint16_t*)a.in)[at]) : ((const float*)a.in)[at];
-          if ((tb[j] >> e) & 1u) z = settle(z, x);
-          if (!((mb[j] >> e) & 1u)) z = -INFINITY;
-          if (BF16) {
-            uint32_t r;
-            asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(r) : "f"(z));
-            ((uint16_t*)a.out)[at] = (uint16_t)r;
-          } else {
-            ((float*)a.out)[at] = z;
+          for (int w = 0; w < W / 4; ++w)
+            p[w] = make_uint4(v[4 * w], v[4 * w + 1], v[4 * w + 2], v[4 * w + 3]);
+        } else if (t0 + 8 > 0 && t0 < a.V) {
+          // a group cut by the row's start or end: token by token
+          for (int e = 0; e < 8; ++e) {
+            const int x = t0 + e;
+            if (x < 0 || x >= a.V) continue;
+            const bool ok = (m >> e) & 1u;
+            if (BF16)
+              ((uint16_t*)a.out)[R[k] + x] = ok ? ((const uint16_t*)a.in)[R[k] + x] : 0xff80u;
+            else
+              ((uint32_t*)a.out)[R[k] + x] = ok ? ((const uint32_t*)a.in)[R[k] + x] : 0xff800000u;
           }
         }
+      }
+    }
+  }
+
+  // ---- the listed tokens: `lanes` threads a token, each with its share of the rows
+  __syncthreads();
+  if (n_touched == 0) return;
+  const int rows = (n - (int)blockIdx.z) / (int)gridDim.z + 1;  // of this CTA
+  const int lanes = min(max(kLgThreads / n_touched, 1), rows);
+  for (int k = tid; k < n_touched * lanes; k += kLgThreads) {
+    const int entry = listed[k % n_touched], x = base + entry;
+    const uint32_t c = cnt[entry], bi = bidx[entry];
+    const float bias = bi ? a.bias_value[br.x + bi - 1] : 0.f;
+    uint64_t nodes = 0;  // that hold this token
+    if (c & 0x40000000u)
+      for (int y = 0; y < nl; ++y)
+        if (node_tok[y] == entry) nodes |= 1ull << node_id[y];
+    for (int q = k / n_touched; q < rows; q += lanes) {
+      const int i = blockIdx.z + q * gridDim.z;
+      const int64_t row = (int64_t)b * (a.Nmax + 1) + i, at = row * a.V + x;
+      // a row that starts inside a group has its first groups' tokens 8 earlier
+      const int group = (x + (int)((row * a.V) & 7)) >> 3;
+      if (group / (kLgSlice / 8) != (int)blockIdx.x) continue;  // another slice streams it
+      if (a.mask) {
+        const int64_t m = a.mask_row ? a.mask_row[row] : row;
+        if (m >= 0 && m < a.n_mask_rows && !((a.mask[m * nw + (x >> 5)] >> (x & 31)) & 1u)) continue;
+      }
+      const uint64_t on = i ? a.anc[(int64_t)b * a.Nmax + i - 1] : 0ull;
+      const uint32_t made = (c & 0x3fffffffu) + __popcll(on & nodes);
+      float z = BF16 ? bf16_to_f32(((const uint16_t*)a.in)[at]) : ((const float*)a.in)[at];
+      if (made || (c >> 31)) z = z > 0.f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
+      if (made) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, (float)made)), pres);
+      if (bi) z = __fadd_rn(z, bias);
+      if (BF16) {
+        uint32_t r;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(r) : "f"(z));
+        ((uint16_t*)a.out)[at] = (uint16_t)r;
+      } else {
+        ((float*)a.out)[at] = z;
       }
     }
   }

@@ -300,7 +300,9 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 // nothing; 1 / 0 (so that 0 * inf = NaN) where all it sees is -infinity.
 __device__ __forceinline__ float row_factor(float l, bool sees) { return sees ? 1.f / l : 0.f; }
 
-// Four 8-bit codes -> two pairs of bf16, exactly.
+// Four 8-bit codes -> bf16, exactly: the codes 0 and 2 in `even`, 1 and 3 in
+// `odd`, which takes fewer instructions than neighbours would (every code is
+// shifted into place within its half word; no bytes are gathered).
 //  e4m3: the sign stays, exponent and mantissa move to the low end of bf16's
 //  fields, which is the value times 2^-120 (subnormal codes become subnormal
 //  bf16); one bf16 product brings it back.  The codes 0x7f and 0xff come out as
@@ -308,22 +310,40 @@ __device__ __forceinline__ float row_factor(float l, bool sees) { return sees ? 
 //  int8: 0x4300 | low 7 bits is 128 + low; minus 128, or 256 where the sign
 //  bit is set.
 template <int CT>
-__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t& even, uint32_t& odd) {
   if constexpr (CT == DT_E4M3) {
-    const uint32_t x = __byte_perm(w, 0, 0x1404), y = __byte_perm(w, 0, 0x3424);
-    const uint32_t u = (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
-    const uint32_t v = (y & 0x80008000u) | ((y >> 4) & 0x07f007f0u);
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(u), "r"(0x7b807b80u));
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(v), "r"(0x7b807b80u));
+    const uint32_t u = ((w << 8) & 0x80008000u) | ((w << 4) & 0x07f007f0u);
+    const uint32_t v = (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u);
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(even) : "r"(u), "r"(0x7b807b80u));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(odd) : "r"(v), "r"(0x7b807b80u));
   } else {
-    const uint32_t x = __byte_perm(w, 0, 0x4140), y = __byte_perm(w, 0, 0x4342);
+    const uint32_t y = w >> 8;
     asm("sub.rn.bf16x2 %0, %1, %2;"
-        : "=r"(lo)
-        : "r"((x & 0x007f007fu) | 0x43004300u), "r"((x & 0x00800080u) | 0x43004300u));
+        : "=r"(even)
+        : "r"((w & 0x007f007fu) | 0x43004300u), "r"((w & 0x00800080u) | 0x43004300u));
     asm("sub.rn.bf16x2 %0, %1, %2;"
-        : "=r"(hi)
+        : "=r"(odd)
         : "r"((y & 0x007f007fu) | 0x43004300u), "r"((y & 0x00800080u) | 0x43004300u));
   }
+}
+
+// mbar_wait with the SM's clock for its limit (about two seconds): the kernels
+// here wait once or twice per key tile, and a look at the global timer takes
+// longer than most of these waits.
+constexpr long long kWaitLimitCycles = 4000000000ll;
+__device__ __forceinline__ bool clock_wait(uint64_t* bar, uint32_t parity, int32_t* status,
+                                           volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort_flag) return false;
+    if (clock64() - t0 > kWaitLimitCycles) {
+      *abort_flag = 1;
+      set_status(status, DT_ETIMEOUT);
+      return false;
+    }
+  }
+  return true;
 }
 
 // One (row, head) by one warp, key by key: 32 keys at a time a lane takes one
@@ -444,6 +464,6 @@ cudaError_t launch_paged_tc(const PagedArgs& a, int ct, const dt_kv_cache* cache
 cudaError_t launch_paged_decode(const PagedArgs& a, int ct, const dt_kv_cache* cache, int pairs,
                                 cudaStream_t s);
 cudaError_t launch_paged_join(const PagedArgs& a, int ct, Cut cut, int workers, cudaStream_t s);
-constexpr int kDecodeWorkers = 11 * kPagedSms, kDecodePairs = 16;
+constexpr int kDecodeWorkers = 15 * kPagedSms, kDecodePairs = 16;  // (the most of any type)
 
 }  // namespace dt

@@ -27,13 +27,14 @@
 namespace dt {
 namespace {
 
-constexpr int kDecWarps = kDecodeWorkers / kPagedSms;
 constexpr float kDecRescale = 8.f;  // log2 units that a maximum may grow without a rescale
 
 template <int D, int CT, int NT>
 struct DecShape {
   static constexpr int kBytes = CT == DT_BF16 ? 2 : 1;
   static constexpr int kKeys = CT == DT_BF16 ? 16 : 32;  // positions of a piece
+  // workers of a CTA: codes take instructions, and more warps hide their latency; bf16 takes bytes
+  static constexpr int kWarps = 11;
   static constexpr int kRow = D * kBytes;                // bytes of a key
   static constexpr int KC = kRow > 128 ? kRow / 128 : 1; // 128-byte columns of the ring
   static constexpr int kWidth = kRow / KC;               // bytes of a row in one of them
@@ -41,9 +42,9 @@ struct DecShape {
   static constexpr bool kScaled = CT != DT_BF16;
   static constexpr int kStage = 2 * kPart;
   static constexpr int kStages = D == 128 ? 2 : 4;
-  static constexpr int kThreads = 32 * (kDecWarps + 1);
+  static constexpr int kThreads = 32 * (kWarps + 1);
   static constexpr int kScaleBytes = kScaled ? 2 * kKeys * 4 : 0;
-  static constexpr size_t kSmem = (size_t)kDecWarps * kStages * (kStage + kScaleBytes + 16) + 1024;
+  static constexpr size_t kSmem = (size_t)kWarps * kStages * (kStage + kScaleBytes + 16) + 1024;
 };
 
 __device__ __forceinline__ void mma_16x8x16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -59,24 +60,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
-}
-
-// Codes of one byte position of two words, as a pair of bf16 (byte x of wa in
-// the low half, of wb in the high half).
-template <int CT, int X>
-__device__ __forceinline__ uint32_t code_pair(uint32_t wa, uint32_t wb) {
-  uint32_t r;
-  if constexpr (CT == DT_E4M3) {
-    const uint32_t v = __byte_perm(wa, wb, (X << 4) | ((4 + X) << 12));  // bytes 1 and 3
-    const uint32_t u = (v & 0x80008000u) | ((v >> 4) & 0x07f007f0u);
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(0x7b807b80u));
-  } else {
-    const uint32_t v = __byte_perm(wa, wb, X | ((4 + X) << 8));  // bytes 0 and 2
-    asm("sub.rn.bf16x2 %0, %1, %2;"
-        : "=r"(r)
-        : "r"((v & 0x007f007fu) | 0x43004300u), "r"((v & 0x00800080u) | 0x43004300u));
-  }
-  return r;
 }
 
 struct DecMaps {
@@ -129,24 +112,24 @@ __global__ void __launch_bounds__(DecShape<D, CT, NT>::kThreads, 1)
   constexpr int ST = S::kStages, KEYS = S::kKeys, KC = S::KC;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  float* scales = (float*)(ring + kDecWarps * ST * S::kStage);  // [worker][stage][K, V][KEYS]
-  uint64_t* bars = (uint64_t*)((uint8_t*)scales + kDecWarps * ST * S::kScaleBytes);
-  int64_t* sums = (int64_t*)(bars + 2 * kDecWarps * ST);        // [batch + 1]
+  float* scales = (float*)(ring + S::kWarps * ST * S::kStage);  // [worker][stage][K, V][KEYS]
+  uint64_t* bars = (uint64_t*)((uint8_t*)scales + S::kWarps * ST * S::kScaleBytes);
+  int64_t* sums = (int64_t*)(bars + 2 * S::kWarps * ST);        // [batch + 1]
   __shared__ volatile int abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Cut cut = {8 * NT, shift};
   pdl_launch_dependents();
   if (tid == 0) {
-    for (int i = 0; i < 2 * kDecWarps * ST; ++i) mbar_init(&bars[i], 1);
+    for (int i = 0; i < 2 * S::kWarps * ST; ++i) mbar_init(&bars[i], 1);
     abort_flag = 0;
     fence_barrier_init();
   }
   const int64_t all = count_units(a, sums, cut);
-  const int workers = (int)min((int64_t)gridDim.x * kDecWarps, all);
+  const int workers = (int)min((int64_t)gridDim.x * S::kWarps, all);
   // neighbouring shares go to different SMs
-  const int w = warp < kDecWarps ? warp : lane;
+  const int w = warp < S::kWarps ? warp : lane;
   const int me = w * gridDim.x + blockIdx.x;
-  const bool busy = w < kDecWarps && me < workers;
+  const bool busy = w < S::kWarps && me < workers;
   const int64_t u0 = busy ? first_unit(all, me, workers) : 0;
   Pieces<KEYS> p;
   p.left = busy ? (int)(first_unit(all, me + 1, workers) - u0) : 0;
@@ -154,12 +137,12 @@ __global__ void __launch_bounds__(DecShape<D, CT, NT>::kThreads, 1)
   uint64_t* empty = full + ST;
   uint8_t* my_ring = ring + w * ST * S::kStage;
   float* my_scales = scales + w * ST * 2 * KEYS;
-  if (warp < kDecWarps && lane == 0) {
+  if (warp < S::kWarps && lane == 0) {
     a.redo[me] = 0;
     if (!busy) a.split[me].parts = 0;
   }
 
-  if (warp == kDecWarps) {
+  if (warp == S::kWarps) {
     // ------------------------------------- the loader: lane w fills worker w's ring
     bool more = busy;
     if (more) {
@@ -169,7 +152,7 @@ __global__ void __launch_bounds__(DecShape<D, CT, NT>::kThreads, 1)
     }
     const int page = 1 << a.c.page_shift, box = min(page, KEYS);
     int n = 0;
-    uint64_t t0 = globaltimer_ns();
+    long long t0 = clock64();
     while (__any_sync(0xffffffffu, more)) {
       if (more && !p.find(a, cut)) {
         more = p.next(a, cut);
@@ -178,7 +161,7 @@ __global__ void __launch_bounds__(DecShape<D, CT, NT>::kThreads, 1)
       if (!more) continue;
       const int st = n % ST;
       if (!mbar_try_wait(&empty[st], ((n / ST) & 1) ^ 1)) {
-        if (abort_flag || globaltimer_ns() - t0 > kWaitLimitNs) {
+        if (abort_flag || clock64() - t0 > kWaitLimitCycles) {
           abort_flag = 1;
           set_status(a.status, DT_ETIMEOUT);
           more = false;
@@ -224,7 +207,7 @@ __global__ void __launch_bounds__(DecShape<D, CT, NT>::kThreads, 1)
       }
       ++n;
       p.at += KEYS;
-      t0 = globaltimer_ns();
+      t0 = clock64();
     }
   } else if (busy) {
     // --------------------------------------------------------------- a worker
@@ -262,8 +245,9 @@ __global__ void __launch_bounds__(DecShape<D, CT, NT>::kThreads, 1)
           else
             at = (t + 4 * (s >> 2)) * 16 + (s & 3) * 4;
           const uint2 x = r < c.t.live ? *(const uint2*)(src + at) : make_uint2(0u, 0u);
-          q[nt][s][0] = x.x;
-          q[nt][s][1] = x.y;
+          // (codes come in pairs 0, 2 and 1, 3 of four)
+          q[nt][s][0] = CT == DT_BF16 ? x.x : __byte_perm(x.x, x.y, 0x5410);
+          q[nt][s][1] = CT == DT_BF16 ? x.y : __byte_perm(x.x, x.y, 0x7632);
         }
       }
       whole_lo = __reduce_max_sync(0xffffffffu, whole_lo);
@@ -283,7 +267,7 @@ __global__ void __launch_bounds__(DecShape<D, CT, NT>::kThreads, 1)
         const uint8_t* vb = kb + S::kPart;
         const float* sc = my_scales + st * 2 * KEYS;
         ok = __all_sync(0xffffffffu,
-                        mbar_wait(&full[st], (n / ST) & 1, a.status, &abort_flag));
+                        clock_wait(&full[st], (n / ST) & 1, a.status, &abort_flag));
         if (!ok) break;
         const bool masked = p.at < whole_lo || p.at + KEYS > whole_hi;
         const bool holes = p.at + KEYS > c.rq.len;
@@ -440,10 +424,16 @@ __global__ void __launch_bounds__(DecShape<D, CT, NT>::kThreads, 1)
             get(r1 + 8, i3);
 #pragma unroll
             for (int y = 0; y < W; ++y) {
-              const uint32_t f[4] = {code_pair<CT, 0>(i0[y], i1[y]), code_pair<CT, 1>(i0[y], i1[y]),
-                                     code_pair<CT, 0>(i2[y], i3[y]), code_pair<CT, 1>(i2[y], i3[y])};
-              const uint32_t h[4] = {code_pair<CT, 2>(i0[y], i1[y]), code_pair<CT, 3>(i0[y], i1[y]),
-                                     code_pair<CT, 2>(i2[y], i3[y]), code_pair<CT, 3>(i2[y], i3[y])};
+              uint32_t e0, e1, e2, e3, d0, d1, d2, d3;
+              codes_to_bf16<CT>(i0[y], e0, d0);
+              codes_to_bf16<CT>(i1[y], e1, d1);
+              codes_to_bf16<CT>(i2[y], e2, d2);
+              codes_to_bf16<CT>(i3[y], e3, d3);
+              // values 0, 1 and 2, 3 of the word, each of two keys
+              const uint32_t f[4] = {__byte_perm(e0, e1, 0x5410), __byte_perm(d0, d1, 0x5410),
+                                     __byte_perm(e2, e3, 0x5410), __byte_perm(d2, d3, 0x5410)};
+              const uint32_t h[4] = {__byte_perm(e0, e1, 0x7632), __byte_perm(d0, d1, 0x7632),
+                                     __byte_perm(e2, e3, 0x7632), __byte_perm(d2, d3, 0x7632)};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 mma_16x8x16(o[nt][2 * y], f, b0[nt], b1[nt]);
@@ -540,7 +530,7 @@ cudaError_t launch_shape(const PagedArgs& a, const DecMaps& maps, int ctas, int 
     if (e != cudaSuccess) return e;
   }
   if (shift == 30) return cudaSuccess;  // one unit a row tile: nothing is cut
-  return launch_paged_join(a, CT, Cut{8 * NT, shift}, ctas * kDecWarps, s);
+  return launch_paged_join(a, CT, Cut{8 * NT, shift}, ctas * S::kWarps, s);
 }
 
 }  // namespace

@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
   int left = cta < shares ? (int)(first_unit(all, cta + 1, shares) - u0) : 0;
   if (cta >= shares && tid == 0) a.split[cta].parts = 0;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return mbar_wait(bar, parity, a.status, abort_flag);
+    return clock_wait(bar, parity, a.status, abort_flag);
   };
   auto wait_item = [&](int n) { return wait(&i_full[n % S::kItems], (n / S::kItems) & 1); };
   auto free_item = [&](int n) { mbar_arrive(&i_empty[n % S::kItems]); };
@@ -552,10 +552,14 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
 #pragma unroll
               for (int i = 0; i < kPieces; ++i) {
                 uint32_t o[8];
-                codes_to_bf16<CT>(w[i].x, o[0], o[1]);
-                codes_to_bf16<CT>(w[i].y, o[2], o[3]);
-                codes_to_bf16<CT>(w[i].z, o[4], o[5]);
-                codes_to_bf16<CT>(w[i].w, o[6], o[7]);
+                const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  uint32_t even, odd;
+                  codes_to_bf16<CT>(in[e], even, odd);
+                  o[2 * e] = __byte_perm(even, odd, 0x5410);
+                  o[2 * e + 1] = __byte_perm(even, odd, 0x7632);
+                }
                 *(uint4*)(dst + to0 + i * kStep * 128) = make_uint4(o[0], o[1], o[2], o[3]);
                 *(uint4*)(dst + to1 + i * kStep * 128) = make_uint4(o[4], o[5], o[6], o[7]);
               }
