@@ -52,22 +52,39 @@ __device__ __forceinline__ uint32_t desc_lo_mn(uint32_t saddr, uint32_t chunk) {
   return ((saddr >> 4) & 0x3FFF) | ((chunk >> 4) << 16);
 }
 
-// D[tmem] (+)= A B, kind::f16, A from shared memory (ss) or TMEM (ts)
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
-                                       uint32_t accumulate) {
+// One lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+  return one;
+}
+// D[tmem] (+)= A B, kind::f16, A from shared memory (ss) or TMEM (ts).  The whole
+// warp comes here and the elected lane (`one`) issues: in code that only one lane
+// runs, every operand would have to be moved to a uniform register first.
+__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint32_t a_lo, uint32_t b_lo,
+                                       uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n"
+      "{\n .reg .pred p, e;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n setp.ne.b32 e, %6, 0;\n"
       " mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d),
-      "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate)
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate), "r"(one)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc,
-                                       uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uint32_t b_lo,
+                                       uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p, e;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n setp.ne.b32 e, %6, 0;\n"
+      " mov.b64 b, {%2, %3};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t one, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+          smem_u32(bar)),
+      "r"(one)
       : "memory");
 }
 
@@ -346,35 +363,26 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
           if (left == 0) break;
           c.next_tile(a, cut);
         }
-      } else if (warp == kWarpMma && lane == 0 && left > 0) {
+      } else if (warp == kWarpMma && left > 0) {
         // ---------------------------------------------------------- the MMAs
         constexpr uint32_t is = idesc_bf16_f32(128, KT);
         constexpr uint32_t io = idesc_bf16_f32(128, D) | (1u << 16);  // B is MN-major
+        const uint32_t one = elect_lane();
         int ns = 0, np = 0;                  // key tiles whose S / O was issued
         uint32_t q_in = 0, p_in = 0;         // phases of q_full and p_full, a bit each
         int ni = 0, in_item = 0, pairs = 0;  // items taken; units left of one, its row tiles
         bool ok = true;
+        auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+          ok = __all_sync(0xffffffffu, ok && wait(bar, parity));
+          tc_fence_after();
+        };
         auto take = [&] {
-          ok = ok && wait_item(ni);
+          wait_all(&i_full[ni % S::kItems], (ni / S::kItems) & 1);
           pairs = items[ni % S::kItems].live > 128 ? 2 : 1;
           in_item = items[ni % S::kItems].seg;
-          free_item(ni++);
-        };
-        auto scores = [&](int q, bool first) {
-          if (first) {
-            ok = ok && wait(&q_full[q], (q_in >> q) & 1);
-            q_in ^= 1u << q;
-            tc_fence_after();
-          }
-          if (!ok) return;
-          const uint32_t qa = desc_lo_k(smem_u32(sq) + q * S::kQTile);
-          const uint32_t ka = desc_lo_k(smem_u32(sk) + ns % ST * S::kTile);
-#pragma unroll
-          for (int s = 0; s < 4 * KC; ++s) {
-            mma_ss(tmem + q * 128, qa + (s >> 2) * (S::kQChunk >> 4) + (s & 3) * 2,
-                   ka + (s >> 2) * (S::kChunk >> 4) + (s & 3) * 2, is, s != 0);
-          }
-          tc_commit(&s_full[q]);
+          __syncwarp();
+          if (one) free_item(ni);
+          ++ni;
         };
         take();
         int live_q = 0, live_next = pairs;
@@ -382,37 +390,44 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
         // turn t: O of unit t - 1, S of unit t
         for (int more = left; ok; --more) {
           const bool pv = live_q > 0, sc = more > 0;
-          if (pv) ok = wait(&v_full[np % ST], (np / ST) & 1);
+          if (pv) wait_all(&v_full[np % ST], (np / ST) & 1);
           const uint32_t va = desc_lo_mn(smem_u32(sv) + np % ST * S::kTile, S::kChunk);
-#pragma unroll 1
+          const uint32_t ka = desc_lo_k(smem_u32(sk) + ns % ST * S::kTile);
+#pragma unroll
           for (int q = 0; q < NQ; ++q) {
             if (q < live_q) {
-              ok = ok && wait(&p_full[q], (p_in >> q) & 1);
+              wait_all(&p_full[q], (p_in >> q) & 1);
               p_in ^= 1u << q;
-              tc_fence_after();
               if (!ok) break;
 #pragma unroll
               for (int s = 0; s < KT / 16; ++s)
-                mma_ts(tmem + NQ * 128 + q * D, tmem + q * 128 + 8 * s, va + 128 * s, io,
+                mma_ts(one, tmem + NQ * 128 + q * D, tmem + q * 128 + 8 * s, va + 128 * s, io,
                        !first || s != 0);
               // (between tiles s_full of the next one says it: it tracks all products so far)
-              if (!sc || first_next) tc_commit(&o_full[q]);
+              if (!sc || first_next) commit_if(one, &o_full[q]);
             }
             if (sc && q < live_next) {
-              if (q == 0) {
-                ok = ok && wait(&k_full[ns % ST], (ns / ST) & 1);
-                tc_fence_after();
+              if (q == 0) wait_all(&k_full[ns % ST], (ns / ST) & 1);
+              if (first_next) {
+                wait_all(&q_full[q], (q_in >> q) & 1);
+                q_in ^= 1u << q;
               }
-              scores(q, first_next);
+              if (!ok) break;
+              const uint32_t qa = desc_lo_k(smem_u32(sq) + q * S::kQTile);
+#pragma unroll
+              for (int s = 0; s < 4 * KC; ++s)
+                mma_ss(one, tmem + q * 128, qa + (s >> 2) * (S::kQChunk >> 4) + (s & 3) * 2,
+                       ka + (s >> 2) * (S::kChunk >> 4) + (s & 3) * 2, is, s != 0);
+              commit_if(one, &s_full[q]);
             }
           }
           if (!ok) break;
           if (pv) {
-            tc_commit(&v_empty[np % ST]);
+            commit_if(one, &v_empty[np % ST]);
             ++np;
           }
           if (!sc) break;
-          tc_commit(&k_empty[ns % ST]);
+          commit_if(one, &k_empty[ns % ST]);
           ++ns;
           live_q = live_next;
           first = first_next;
