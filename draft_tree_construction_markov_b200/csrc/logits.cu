@@ -83,6 +83,8 @@ __global__ void __launch_bounds__(kLgThreads) logits_kernel(LogitsArgs a) {
   __shared__ uint16_t listed[kLgTab];            // table entries that something touches
   __shared__ int node_tok[64], node_id[64];
   __shared__ int n_nodes_here, n_listed;
+  __shared__ int row_mask[65];                   // mask row of row i, -1: everything allowed
+  __shared__ uint64_t row_path[65];              // its ancestor word
   const int tid = threadIdx.x, b = blockIdx.y;
   const int base = blockIdx.x * kLgSlice - 8;  // token of table entry 0
   int n = 0;
@@ -98,6 +100,19 @@ __global__ void __launch_bounds__(kLgThreads) logits_kernel(LogitsArgs a) {
   // ---- the slice's table
   for (int i = tid; i < kLgTab; i += kLgThreads) cnt[i] = bidx[i] = 0;
   if (tid == 0) n_nodes_here = n_listed = 0;
+  if (tid <= n) {
+    const int64_t row = (int64_t)b * (a.Nmax + 1) + tid;
+    int m = -1;
+    if (a.mask) {
+      m = a.mask_row ? a.mask_row[row] : (int)min(row, (int64_t)INT_MAX);
+      if (m < -1 || m >= a.n_mask_rows) {
+        set_status(a.status, DT_EDEVICE);
+        m = -1;
+      }
+    }
+    row_mask[tid] = m;
+    row_path[tid] = tid ? a.anc[row - b - 1] : 0ull;  // b * Nmax + tid - 1
+  }
   __syncthreads();
   if (a.hist) {
     const int2 r = list_range(a.hist_start, b, a.n_hist, a.status);
@@ -165,23 +180,11 @@ __global__ void __launch_bounds__(kLgThreads) logits_kernel(LogitsArgs a) {
   for (int i0 = blockIdx.z; i0 <= n; i0 += RB * gridDim.z) {
     int64_t R[RB];            // first element of row k
     const uint32_t* mask[RB];
-    int mrow[RB];
 #pragma unroll
     for (int k = 0; k < RB; ++k) {
-      const int i = i0 + k * gridDim.z;
-      const int64_t row = (int64_t)b * (a.Nmax + 1) + i;
-      R[k] = row * a.V;
-      mrow[k] = -1;
-      if (a.mask && i <= n) mrow[k] = a.mask_row ? a.mask_row[row] : (int)min(row, (int64_t)INT_MAX);
-    }
-#pragma unroll
-    for (int k = 0; k < RB; ++k) {
-      mask[k] = nullptr;
-      if (mrow[k] < -1 || mrow[k] >= a.n_mask_rows) {
-        if (tid == 0 && (a.mask && i0 + k * (int)gridDim.z <= n)) set_status(a.status, DT_EDEVICE);
-      } else if (mrow[k] >= 0) {
-        mask[k] = a.mask + (int64_t)mrow[k] * nw;
-      }
+      const int i = min(i0 + k * (int)gridDim.z, n);
+      R[k] = ((int64_t)b * (a.Nmax + 1) + i) * a.V;
+      mask[k] = row_mask[i] >= 0 ? a.mask + (int64_t)row_mask[i] * nw : nullptr;
     }
     uint32_t u[RB][kLgGroups][W];
     uint32_t mb[RB][kLgGroups];
@@ -267,28 +270,42 @@ __global__ void __launch_bounds__(kLgThreads) logits_kernel(LogitsArgs a) {
     if (c & 0x40000000u)
       for (int y = 0; y < nl; ++y)
         if (node_tok[y] == entry) nodes |= 1ull << node_id[y];
-    for (int q = k / n_touched; q < rows; q += lanes) {
-      const int i = blockIdx.z + q * gridDim.z;
-      const int64_t row = (int64_t)b * (a.Nmax + 1) + i, at = row * a.V + x;
-      // a row that starts inside a group has its first groups' tokens 8 earlier
-      const int group = (x + (int)((row * a.V) & 7)) >> 3;
-      if (group / (kLgSlice / 8) != (int)blockIdx.x) continue;  // another slice streams it
-      if (a.mask) {
-        const int64_t m = a.mask_row ? a.mask_row[row] : row;
-        if (m >= 0 && m < a.n_mask_rows && !((a.mask[m * nw + (x >> 5)] >> (x & 31)) & 1u)) continue;
+    // (rows four at a time: their masks and logits are on their way together)
+    for (int q0 = k / n_touched; q0 < rows; q0 += 4 * lanes) {
+      float z4[4];
+      bool ok[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int q = q0 + y * lanes, i = blockIdx.z + min(q, rows - 1) * gridDim.z;
+        const int64_t R = ((int64_t)b * (a.Nmax + 1) + i) * a.V;
+        // groups begin up to 7 tokens before the row: the token may be another slice's
+        const int group = (x + (int)(R & 7)) >> 3;
+        ok[y] = q < rows && group / (kLgSlice / 8) == (int)blockIdx.x;
+        z4[y] = 0.f;
+        if (ok[y]) {
+          const int m = row_mask[i];
+          const uint32_t word = m >= 0 ? a.mask[(int64_t)m * nw + (x >> 5)] : 0xffffffffu;
+          z4[y] = BF16 ? bf16_to_f32(((const uint16_t*)a.in)[R + x]) : ((const float*)a.in)[R + x];
+          ok[y] = (word >> (x & 31)) & 1u;
+        }
       }
-      const uint64_t on = i ? a.anc[(int64_t)b * a.Nmax + i - 1] : 0ull;
-      const uint32_t made = (c & 0x3fffffffu) + __popcll(on & nodes);
-      float z = BF16 ? bf16_to_f32(((const uint16_t*)a.in)[at]) : ((const float*)a.in)[at];
-      if (made || (c >> 31)) z = z > 0.f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
-      if (made) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, (float)made)), pres);
-      if (bi) z = __fadd_rn(z, bias);
-      if (BF16) {
-        uint32_t r;
-        asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(r) : "f"(z));
-        ((uint16_t*)a.out)[at] = (uint16_t)r;
-      } else {
-        ((float*)a.out)[at] = z;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        if (!ok[y]) continue;
+        const int i = blockIdx.z + (q0 + y * lanes) * gridDim.z;
+        const int64_t at = ((int64_t)b * (a.Nmax + 1) + i) * a.V + x;
+        const uint32_t made = (c & 0x3fffffffu) + __popcll(row_path[i] & nodes);
+        float z = z4[y];
+        if (made || (c >> 31)) z = z > 0.f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
+        if (made) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, (float)made)), pres);
+        if (bi) z = __fadd_rn(z, bias);
+        if (BF16) {
+          uint32_t r;
+          asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(r) : "f"(z));
+          ((uint16_t*)a.out)[at] = (uint16_t)r;
+        } else {
+          ((float*)a.out)[at] = z;
+        }
       }
     }
   }

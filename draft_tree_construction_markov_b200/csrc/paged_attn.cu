@@ -29,17 +29,13 @@ __global__ void __launch_bounds__(32 * kPlainWarps) paged_plain_kernel(PagedArgs
   if (i < paged_request(a, b).n && h < a.Hq) paged_row<CT, DT>(a, b, i, h);
 }
 
-// Joins the shares of a row tile.  grid (workers of the tiled kernel, row parts);
-// a warp takes a row, its lanes four columns each.
-constexpr int kJoinWarps = 8, kJoinRows = 32;
-
-// Rows that worker blockIdx.x finished and that came out infinite or NaN: again,
-// key by key (see paged_row).
+// Rows that worker `me` finished and that came out infinite or NaN: again, key by
+// key (see paged_row).
 template <int CT>
-__device__ __noinline__ void join_redo(const PagedArgs& a, Cut cut) {
+__device__ __noinline__ void join_redo(const PagedArgs& a, Cut cut, int me, int most) {
   __shared__ int64_t sums[kMaxKvBatch + 1];
   const int64_t all = count_units(a, sums, cut);
-  const int workers = (int)min((int64_t)gridDim.x, all), me = blockIdx.x;
+  const int workers = (int)min((int64_t)most, all);
   if (me >= workers) return;
   const int64_t u0 = first_unit(all, me, workers);
   int64_t left = first_unit(all, me + 1, workers) - u0;
@@ -47,8 +43,7 @@ __device__ __noinline__ void join_redo(const PagedArgs& a, Cut cut) {
   Cursor c;
   for (c.seek(a, sums, u0, cut);; c.next_tile(a, cut)) {
     if (c.u == 0 && c.t.units <= left) {
-      for (int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
-           r < min(c.t.live, (int)(blockIdx.y + 1) * kJoinRows); r += kJoinWarps) {
+      for (int r = threadIdx.x >> 5; r < c.t.live; r += kJoinWarps) {
         const int i = (c.t.m0 + r) / a.G, h = c.kvh * a.G + (c.t.m0 + r) % a.G;
         const uint16_t* out = (const uint16_t*)a.out + (((int64_t)c.rq.r0 + i) * a.Hq + h) * a.d;
         bool odd = false;
@@ -59,55 +54,132 @@ __device__ __noinline__ void join_redo(const PagedArgs& a, Cut cut) {
     left -= c.t.units - c.u;
     if (left <= 0) break;
   }
+  __syncthreads();
 }
 
+// Joins the shares of row tiles.  The tasks of all workers are a list that the
+// blocks share out (most workers have few or none, one may have hundreds); every
+// block adds the list up for itself.  A warp has its row's statistics and the
+// first parts' sums on the way together, its lanes four columns each.
 template <int CT>
 __global__ void __launch_bounds__(32 * kJoinWarps)
-    paged_join_kernel(const __grid_constant__ PagedArgs a, Cut cut) {
+    paged_join_kernel(const __grid_constant__ PagedArgs a, Cut cut, int workers) {
+  __shared__ float4 sums[kJoinWarps][32];
+  __shared__ int before[kDecodeWorkers + 1];  // tasks before worker w
+  __shared__ int carry[kJoinWarps];
   pdl_wait();
-  if (a.redo[blockIdx.x]) join_redo<CT>(a, cut);
-  const PagedSplit sp = a.split[blockIdx.x];
-  if (sp.parts == 0) return;
-  const PagedRequest rq = paged_request(a, sp.b);
-  const RowTile t = row_tile(a, rq, sp.mt, cut);
-  const int lane = threadIdx.x & 31;
-  for (int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
-       r < min(t.live, (int)(blockIdx.y + 1) * kJoinRows); r += kJoinWarps) {
-    const int i = (t.m0 + r) / a.G, h = sp.kvh * a.G + (t.m0 + r) % a.G;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  bool redo = false;
+  constexpr int kPer = (kDecodeWorkers + 32 * kJoinWarps - 1) / (32 * kJoinWarps);
+  {
+    int t[kPer], sum = 0;
+#pragma unroll
+    for (int y = 0; y < kPer; ++y) {
+      const int w = threadIdx.x * kPer + y;
+      t[y] = w < workers ? a.tasks[w] : 0;
+      redo |= w < workers && a.redo[w];
+    }
+#pragma unroll
+    for (int y = 0; y < kPer; ++y) sum += t[y];
+    int x = sum;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += v;
+    }
+    if (lane == 31) carry[warp] = x;
+    redo = __syncthreads_or(redo);
+    int at = x - sum;
+    for (int y = 0; y < warp; ++y) at += carry[y];
+#pragma unroll
+    for (int y = 0; y < kPer; ++y) {
+      const int w = threadIdx.x * kPer + y;
+      if (w <= workers) before[w] = at;
+      at += t[y];
+    }
+    __syncthreads();
+  }
+  if (redo)
+    for (int w = blockIdx.x; w < workers; w += gridDim.x)
+      if (a.redo[w]) join_redo<CT>(a, cut, w, workers);
+  const bool col = lane * 4 < a.d;
+  for (int task = blockIdx.x; task < before[workers]; task += gridDim.x) {
+    int lo = 0, hi = workers;  // before[lo] <= task < before[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before[mid] <= task)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    const PagedSplit sp = a.split[lo];
+    const int share = join_share(sp.parts), mine = warp % share;
+    const int r = (task - before[lo]) * (kJoinWarps / share) + warp / share;
+    const bool there = r < sp.live;
     // part 0: the second slot of the worker before; part k: the first slot of worker + k - 1
     auto at = [&](int k) {
-      const int64_t slot = k ? 2 * ((int64_t)blockIdx.x + k - 1) : 2 * (int64_t)blockIdx.x - 1;
+      const int64_t slot = k ? 2 * ((int64_t)lo + k - 1) : 2 * (int64_t)lo - 1;
       return slot * a.part_rows + r;
     };
     float m = -INFINITY, l = 0.f;
-    for (int k = lane; k < sp.parts; k += 32) m = fmaxf(m, a.part_ml[at(k)].x);
-    m = warp_max(m);
-    for (int k = lane; k < sp.parts; k += 32) {
-      const float2 ml = a.part_ml[at(k)];
-      l += ml.x == -INFINITY ? ml.y : ex2(ml.x - m) * ml.y;  // (a NaN sum stays one)
-    }
-    l = warp_sum(l);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (lane * 4 < a.d) {
-#pragma unroll 4
-      for (int k = 0; k < sp.parts; ++k) {
-        const float mk = a.part_ml[at(k)].x;
-        const float w = mk == -INFINITY ? 0.f : ex2(mk - m);
-        const float4 x = *(const float4*)(a.part_o + at(k) * a.d + lane * 4);
-        o.x = fmaf(w, x.x, o.x);
-        o.y = fmaf(w, x.y, o.y);
-        o.z = fmaf(w, x.z, o.z);
-        o.w = fmaf(w, x.w, o.w);
+    if (there) {
+      constexpr int kAhead = 6;  // parts on their way
+      float w[kAhead];
+      float4 x[kAhead];
+      auto ask = [&](int k0) {
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) {
+          const int k = k0 + y * share;
+          w[y] = -INFINITY;
+          x[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k < sp.parts) {
+            w[y] = a.part_ml[at(k)].x;
+            if (col) x[y] = *(const float4*)(a.part_o + at(k) * a.d + lane * 4);
+          }
+        }
+      };
+      ask(mine);
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (lane < sp.parts) ml = a.part_ml[at(lane)];
+      m = ml.x;
+      for (int k = 32 + lane; k < sp.parts; k += 32) m = fmaxf(m, a.part_ml[at(k)].x);
+      m = warp_max(m);
+      auto weigh = [&](float2 p) {  // (a NaN sum stays one)
+        l += p.x == -INFINITY ? p.y : ex2(p.x - m) * p.y;
+      };
+      weigh(ml);
+      for (int k = 32 + lane; k < sp.parts; k += 32) weigh(a.part_ml[at(k)]);
+      l = warp_sum(l);
+      for (int k0 = mine; k0 < sp.parts; k0 += kAhead * share) {
+        if (k0 != mine) ask(k0);
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) {
+          const float f = w[y] == -INFINITY ? 0.f : ex2(w[y] - m);
+          o.x = fmaf(f, x[y].x, o.x);
+          o.y = fmaf(f, x[y].y, o.y);
+          o.z = fmaf(f, x[y].z, o.z);
+          o.w = fmaf(f, x[y].w, o.w);
+        }
       }
     }
-    const Visible vis = visible(a, row_position(a, rq, sp.b, i), rq.len);
-    const bool sees = a.kt || vis.sink > 0 || vis.last > vis.first;
+    if (share > 1) {
+      __syncthreads();
+      sums[warp][lane] = o;
+      __syncthreads();
+      for (int y = 1; mine == 0 && y < share; ++y) {
+        const float4 x = sums[warp + y][lane];
+        o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+      }
+    }
+    if (!there || mine) continue;
+    const int i = (sp.m0 + r) / a.G, h = sp.kvh * a.G + (sp.m0 + r) % a.G;
+    const bool sees = !(l < 0.f);
     const float inv = row_factor(l, sees);
-    if (lane * 4 < a.d)
-      *(uint2*)((uint16_t*)a.out + (((int64_t)rq.r0 + i) * a.Hq + h) * a.d + lane * 4) =
+    if (col)
+      *(uint2*)((uint16_t*)a.out + (((int64_t)sp.r0 + i) * a.Hq + h) * a.d + lane * 4) =
           sees ? make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv))
                : make_uint2(0u, 0u);
-    const float odd = (o.x + o.y + o.z + o.w) * 0.f;
+    const float odd = o.x * 0.f + o.y * 0.f + o.z * 0.f + o.w * 0.f;
     if (__any_sync(0xffffffffu, sees && odd != 0.f && l - l == 0.f))
       paged_row<CT, DT_BF16>(a, sp.b, i, h);
   }
@@ -134,12 +206,13 @@ EncodeFn encode_fn() {
 // Records, fp32 sums and statistics of the row tiles that shares cut, two per
 // worker; `all`: (row, head) pairs of a KV head that a row tile can have at most.
 struct PartPlan {
-  size_t redo, sums, stats, bytes;  // offsets behind the header, and all
+  size_t redo, tasks, sums, stats, bytes;  // offsets behind the header, and all
 };
 PartPlan part_plan(int64_t workers, int64_t rows, int d) {
   PartPlan p;
-  p.redo = workers * sizeof(PagedSplit);
-  p.sums = p.redo + ((workers * 4 + 15) & ~(size_t)15);
+  p.redo = (workers * sizeof(PagedSplit) + 15) & ~(size_t)15;
+  p.tasks = p.redo + workers * 4;
+  p.sums = p.redo + ((workers * 8 + 15) & ~(size_t)15);
   p.stats = p.sums + 2 * workers * rows * d * 4;
   p.bytes = kWsHeader + p.stats + 2 * workers * rows * sizeof(float2);
   return p;
@@ -177,6 +250,7 @@ dt_status run_paged(PagedArgs a, const dt_kv_cache* cache, int dt, void* ws, cud
   uint8_t* w = (uint8_t*)ws + kWsHeader;
   a.split = (PagedSplit*)w;
   a.redo = (int*)(w + p.redo);
+  a.tasks = (int*)(w + p.tasks);
   a.part_o = (float*)(w + p.sums);
   a.part_ml = (float2*)(w + p.stats);
   const cudaError_t e = few ? launch_paged_decode(a, ct, cache, (int)pairs, s)
@@ -215,11 +289,11 @@ bool paged_map(CUtensorMap* m, const void* base, int bytes, uint64_t cols, uint6
 
 cudaError_t launch_paged_join(const PagedArgs& a, int ct, Cut cut, int workers, cudaStream_t s) {
   ProfileScope ps(DT_K_ATTN_COMBINE, s);
-  const dim3 grid(workers, (a.part_rows + kJoinRows - 1) / kJoinRows);
+  const dim3 grid(std::min(4 * dt_num_sms(), std::max(workers, 1) * a.part_rows));
   auto kern = ct == DT_BF16   ? paged_join_kernel<DT_BF16>
               : ct == DT_E4M3 ? paged_join_kernel<DT_E4M3>
                               : paged_join_kernel<DT_I8>;
-  const cudaError_t e = launch_pdl(kern, grid, dim3(32 * kJoinWarps), 0, s, a, cut);
+  const cudaError_t e = launch_pdl(kern, grid, dim3(32 * kJoinWarps), 0, s, a, cut, workers);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 

@@ -29,7 +29,8 @@ struct PagedArgs {
   // split-and-join workspace (PagedSplit)
   struct PagedSplit* split;
   int* redo;        // [workers]: some finished row came out infinite or NaN
-  float2* part_ml;  // [2 * workers][part_rows]: (max in log2 units, sum)
+  int* tasks;       // [workers]: tasks of the join (join_tasks)
+  float2* part_ml;  // [2 * workers][part_rows]: (max in log2 units, sum; -1: the row sees nothing)
   float* part_o;    // [2 * workers][part_rows][d], not yet divided by the sum
   int part_rows;
 };
@@ -258,20 +259,30 @@ __device__ __forceinline__ int64_t first_unit(int64_t all, int c, int n) {
 
 // Written by the worker that meets a row tile's second share: where to join.
 struct PagedSplit {
-  int parts;  // 0: nothing to join here
-  int b, kvh, mt;
+  int parts;             // 0: nothing to join here
+  int b, kvh, m0, live;  // the row tile
+  int r0;                // first row of its request
 };
+
+// The join has 8 warps a block; `share` of them take a row of `parts` parts, and
+// a block as many rows at once as that leaves: a task.
+constexpr int kJoinWarps = 8;
+__host__ __device__ __forceinline__ int join_share(int parts) {
+  return parts <= 6 ? 1 : parts <= 12 ? 2 : parts <= 24 ? 4 : 8;
+}
 
 // Every worker, one thread: records what starts in the share before its own.
 __device__ __forceinline__ void record_split(const PagedArgs& a, const Cursor& c, int64_t all,
                                              int me, int n) {
-  PagedSplit s = {0, c.b, c.kvh, c.mt};
+  PagedSplit s = {0, c.b, c.kvh, c.t.m0, c.t.live, c.rq.r0};
   const int64_t at = first_unit(all, me, n), from = at - c.u, to = from + c.t.units;
   if (me > 0 && c.u > 0 && first_unit(all, me - 1, n) <= from) {
     s.parts = 1;
     for (int k = me; k < n && first_unit(all, k, n) < to; ++k) ++s.parts;
   }
   a.split[me] = s;
+  const int rows = kJoinWarps / join_share(s.parts);
+  a.tasks[me] = s.parts ? (s.live + rows - 1) / rows : 0;
 }
 
 __device__ __forceinline__ float ex2(float x) {

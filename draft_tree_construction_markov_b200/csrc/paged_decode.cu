@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(DecShape<D, CT, NT>::kThreads, 1)
   float* my_scales = scales + w * ST * 2 * KEYS;
   if (warp < S::kWarps && lane == 0) {
     a.redo[me] = 0;
-    if (!busy) a.split[me].parts = 0;
+    if (!busy) a.tasks[me] = 0;
   }
 
   if (warp == S::kWarps) {
@@ -460,10 +460,9 @@ __global__ void __launch_bounds__(DecShape<D, CT, NT>::kThreads, 1)
           const bool there = r < c.t.live;
           // this thread's values of row r: groups of eight neighbouring columns
           constexpr int kGroups = D / 64;
+          const bool sees = vis[nt][e].sink > 0 || vis[nt][e].last > vis[nt][e].first;
           if (whole) {
             const int mm = c.t.m0 + (there ? r : 0);
-            const Visible& v = vis[nt][e];
-            const bool sees = v.sink > 0 || v.last > v.first;
             const float inv = row_factor(sum, sees);
             uint16_t* out = (uint16_t*)a.out + ((c.rq.r0 + (int64_t)(mm / a.G)) * a.Hq +
                                                 (int64_t)c.kvh * a.G + mm % a.G) * D;
@@ -487,7 +486,7 @@ __global__ void __launch_bounds__(DecShape<D, CT, NT>::kThreads, 1)
               if (bad & (0x11111111u << x)) again |= 1u << (nt * 8 + 2 * x + e);
           } else if (there) {
             const int64_t at = (int64_t)(2 * me + (head ? 0 : 1)) * a.part_rows + r;
-            if (g == 0) a.part_ml[at] = make_float2(m[nt][e], sum);
+            if (g == 0) a.part_ml[at] = make_float2(m[nt][e], sees ? sum : -1.f);
 #pragma unroll
             for (int y = 0; y < kGroups; ++y) {
               float* po = a.part_o + at * D + (CT == DT_BF16 ? y * 64 + g * 8 : g * (D / 8) + y * 8);

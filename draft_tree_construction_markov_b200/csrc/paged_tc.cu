@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
   const int shares = (int)min((int64_t)gridDim.x, all), cta = blockIdx.x;
   const int64_t u0 = cta < shares ? first_unit(all, cta, shares) : 0;
   int left = cta < shares ? (int)(first_unit(all, cta + 1, shares) - u0) : 0;
-  if (cta >= shares && tid == 0) a.split[cta].parts = 0;
+  if (cta >= shares && tid == 0) a.tasks[cta] = 0;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return clock_wait(bar, parity, a.status, abort_flag);
   };
@@ -931,7 +931,7 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
       } else {
         const int64_t at = (int64_t)(2 * cta + (head ? 0 : 1)) * a.part_rows + q * 128 + row;
         float* po = a.part_o + at * D;
-        if (there) a.part_ml[at] = make_float2(m, l);
+        if (there) a.part_ml[at] = make_float2(m, sees ? l : -1.f);
 #pragma unroll 1
         for (int w = 0; w < D / 32; ++w) {
           uint32_t r[32];
