@@ -29,7 +29,7 @@ constexpr int kLgSlice = 4096;                 // tokens per CTA
 constexpr int kLgTab = kLgSlice + 8;           // rows start up to 7 tokens into a group of 8
 constexpr int kLgGroups = kLgSlice / 8 / kLgThreads;  // groups per thread and row
 template <bool BF16>
-constexpr int kLgRows = BF16 ? 4 : 2;                 // rows at a time
+constexpr int kLgRows = BF16 ? 2 : 1;                 // rows at a time
 
 struct LogitsArgs {
   const void* in;
@@ -76,7 +76,7 @@ __device__ __forceinline__ int2 list_range(const int32_t* start, int b, int n, i
 
 // grid (slices, batch, row groups)
 template <bool BF16, bool INPLACE>
-__global__ void __launch_bounds__(kLgThreads) logits_kernel(LogitsArgs a) {
+__global__ void __launch_bounds__(kLgThreads, 5) logits_kernel(LogitsArgs a) {
   constexpr int W = BF16 ? 4 : 8;  // 32-bit words of a group of 8 tokens
   __shared__ uint32_t cnt[kLgTab];
   __shared__ uint32_t bidx[kLgTab];
@@ -227,13 +227,12 @@ __global__ void __launch_bounds__(kLgThreads) logits_kernel(LogitsArgs a) {
         if (t0 >= 0 && t0 + 8 <= a.V) {
           if (m != 0xffu) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int w = 0; w < W; ++w) {
               if (BF16) {
-                if (!((m >> e) & 1u))
-                  v[e >> 1] = (e & 1) ? (v[e >> 1] & 0x0000ffffu) | 0xff800000u
-                                      : (v[e >> 1] & 0xffff0000u) | 0x0000ff80u;
-              } else if (!((m >> e) & 1u)) {
-                v[e] = 0xff800000u;
+                const uint32_t keep = (m >> (2 * w) & 1u) * 0xffffu | (m >> (2 * w + 1) & 1u) * 0xffff0000u;
+                v[w] = (v[w] & keep) | (0xff80ff80u & ~keep);
+              } else if (!((m >> w) & 1u)) {
+                v[w] = 0xff800000u;
               }
             }
           }
@@ -370,8 +369,10 @@ dt_status dt_logits_process(const void* d_logits, dt_dtype dt, const int32_t* d_
   // a row may start 7 tokens into its first group of 8
   const int slices = (V + 7 + kLgSlice - 1) / kLgSlice;
   const int rows = Nmax + 1;
-  // rows are split over CTAs until there are about six per SM
-  const int want = (6 * dt_num_sms() + slices * batch - 1) / (slices * batch);
+  // Rows are split over CTAs until there are about 16 per SM: trees differ in
+  // size, and the rows of the largest are what the call waits for.  Against that
+  // every CTA of a slice counts the history anew.
+  const int want = (16 * dt_num_sms() + slices * batch - 1) / (slices * batch);
   const int z = want < 1 ? 1 : want > rows ? rows : want;
   const dim3 grid(slices, batch, z);
   cudaStream_t s = (cudaStream_t)stream;
