@@ -109,25 +109,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(taddr)
       : "memory");
 }
-// 16 rows x 32 columns, the layout of an mma.sync fragment: lane 4 i + j holds
-// columns 8 k + 2 j, 8 k + 2 j + 1 of row i in r[4 k], r[4 k + 1] and of row
-// i + 8 in r[4 k + 2], r[4 k + 3].
-__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-// The same fragment as pairs of 16-bit values: r[2 k] row i, r[2 k + 1] row i + 8.
-__device__ __forceinline__ void tmem_st_frag16(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -219,8 +200,9 @@ struct TcShape {
   static constexpr int kStages = kTma && (NQ == 2 || D == 64) ? 2 : 1;
   static constexpr int kCodes = 4, kCodeBytes = KT * D;
   static constexpr int kScales = 4;             // tiles of row scales (see the loader)
-  // 32-column parts of S that a row keeps in registers between its two passes (bf16 caches)
-  static constexpr int kKeep = NQ == 2 ? 4 : 2;
+  // 32-column parts of S that a row keeps in registers between its two passes: all of them, or
+  // one at a time, read twice (TMEM gives 32 columns in 27 cycles; a spill costs more)
+  static constexpr int kKeep = kTma && NQ == 2 ? 4 : 1;
   // Where registers are scarce the warps come in whole warpgroups and deal them
   // out anew: more for the softmax (S in registers), less for the others.  (A
   // function call in the kernel would undo this: the compiler then allots the
@@ -249,7 +231,7 @@ struct TcShape {
   static constexpr int kRows = 128 * NQ;
   static constexpr int kBars = 4 * kStages + 4 * NQ + kScales + 2 * kCodes + 2 * kItems;
   static constexpr size_t kCoded =
-      kTma ? 0 : (size_t)kCodes * kCodeBytes + kScales * (2 * KT * 4) + kSoft * 16;
+      kTma ? 0 : (size_t)kCodes * kCodeBytes + kScales * (2 * KT * 4);
   static constexpr size_t kSmem = (size_t)NQ * kQTile + 2 * kStages * kTile + kCoded +
                                   kItems * sizeof(Item) + kBars * 8 + 16 + 1024;
 };
@@ -269,11 +251,10 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
   uint8_t* sq = smem;                              // Q [NQ][KC][128 rows][128 B]
   uint8_t* sk = sq + NQ * S::kQTile;               // K [ST][KC][KT keys][128 B]
   uint8_t* sv = sk + ST * S::kTile;                // V [ST][KC][KT keys][128 B]
-  // 8-bit caches: halves of tiles (keys, values) as codes, scales of tiles, what each row sees
+  // 8-bit caches: halves of tiles (keys, values) as codes, scales of tiles
   uint8_t* scode = (uint8_t*)(sv + ST * S::kTile);                       // [kCodes][KT][D]
   float* sscale = (float*)(scode + (S::kTma ? 0 : S::kCodes * S::kCodeBytes));  // [kScales][K, V][KT]
-  uint4* smask = (uint4*)(sscale + (S::kTma ? 0 : S::kScales * 2 * KT));        // [rows]
-  Item* items = (Item*)(smask + (S::kTma ? 0 : S::kSoft));               // [kItems]
+  Item* items = (Item*)(sscale + (S::kTma ? 0 : S::kScales * 2 * KT));   // [kItems]
   uint64_t* bars = (uint64_t*)(items + S::kItems);
   uint64_t* k_full = bars;
   uint64_t* k_empty = k_full + ST;
@@ -662,9 +643,7 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
       // key tiles in [whole_lo, whole_hi) need no mask for any row of the warp
       const int whole_lo = __reduce_max_sync(0xffffffffu, mask.vis.first);
       const int whole_hi = __reduce_min_sync(0xffffffffu, mask.vis.last);
-      float m = -INFINITY, l = 0.f;  // (bf16 cache) this thread's row
-      // (8-bit cache) rows lane / 4 + 8 x of the warp; each sum is that of this lane's columns
-      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, l4[4] = {0.f, 0.f, 0.f, 0.f};
+      float m = -INFINITY, l = 0.f;
       // O times a factor per row: the products so far are complete (s_full)
       auto rescale = [&](float keep) {
 #pragma unroll 1
@@ -693,14 +672,28 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
           q_started = items[(n + 1) % S::kItems].live > q * 128;
           if (q_started) start_q(n + 1);
         }
-        if constexpr (S::kTma) {
-          constexpr int kKeep = S::kKeep;
+        {
+          constexpr int kKeep = S::kKeep, kParts = KT / 32;
+          // (a scale of NaN at a place that a row does not see makes its sum NaN, with a
+          // finite weight sum: such rows are done again, see paged_row)
+          const float* scales = sscale + g % S::kScales * 2 * KT;
           // ---- the row's largest score of this tile
           uint32_t r[kKeep][32];
           auto load = [&](int w0) {
 #pragma unroll
             for (int w = w0; w < w0 + kKeep; ++w) tmem_ld32(ts + 32 * w, r[w - w0]);
             tmem_wait_ld();
+            if constexpr (!S::kTma) {  // times the keys' scales
+#pragma unroll
+              for (int w = w0; w < w0 + kKeep; ++w)
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                  const float4 f = *(const float4*)(scales + 32 * w + e);
+                  uint32_t* x = r[w - w0] + e;
+                  mul2(x[0], x[1], f.x, f.y);
+                  mul2(x[2], x[3], f.z, f.w);
+                }
+            }
             if (masked) {
 #pragma unroll
               for (int w = w0; w < w0 + kKeep; ++w) {
@@ -712,9 +705,8 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
             }
           };
           float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          // the first parts are read twice where not all of them fit the registers
-#pragma unroll
-          for (int w0 = 4 - kKeep; w0 >= 0; w0 -= kKeep) {
+#pragma unroll 1
+          for (int w0 = kParts - kKeep; w0 >= 0; w0 -= kKeep) {
             load(w0);
 #pragma unroll
             for (int w = 0; w < kKeep; ++w)
@@ -737,13 +729,13 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
           const float less = m == -INFINITY ? 0.f : -m;
           // ---- weights, in bf16 for the second product, over the scores
           float la[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            if (w > 0 && w % kKeep == 0) load(w);
+#pragma unroll (kKeep == 1 ? 1 : kParts)
+          for (int w = 0; w < kParts; ++w) {
+            if (kKeep == 1) load(w);
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
-              uint32_t* x = r[w % kKeep] + e;
+              uint32_t* x = r[kKeep == 1 ? 0 : w] + e;
               float p[4];
               fma2(x[0], x[1], sl2, less, p[0], p[1]);
               fma2(x[2], x[3], sl2, less, p[2], p[3]);
@@ -751,12 +743,24 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
               for (int y = 0; y < 4; ++y) p[y] = ex2(p[y]);
               add2(la[0], la[1], p[0], p[1]);
               add2(la[2], la[3], p[2], p[3]);
+              if constexpr (!S::kTma) {  // times the values' scales
+                const float4 f = *(const float4*)(scales + KT + 32 * w + e);
+                uint32_t z[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) z[y] = __float_as_uint(p[y]);
+                mul2(z[0], z[1], f.x, f.y);
+                mul2(z[2], z[3], f.z, f.w);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) p[y] = __uint_as_float(z[y]);
+              }
               pk[e / 2] = pack2(p[0], p[1]);
               pk[e / 2 + 1] = pack2(p[2], p[3]);
             }
             tmem_st16(ts + 16 * w, pk);
           }
           l += (la[0] + la[1]) + (la[2] + la[3]);
+        }
+        if constexpr (S::kTma) {
           // V rows that are no positions of the request may hold anything: zeros, before 0 * NaN
           const int valid = base < 0 ? rq.n : rq.len - base;
           if (valid < KT) {
@@ -771,115 +775,6 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
             }
             fence_async_smem();
           }
-        } else {
-          // The keys' scales multiply columns, and a thread of a whole row would
-          // read each of them: 3 x 128 shared loads a tile that all lanes repeat.
-          // In fragment layout a lane has a quarter of the columns of four rows.
-          // (A scale of NaN at a place that a row does not see makes its sum NaN,
-          // with a finite weight sum: such rows are done again, see paged_row.)
-          const float* kscale = sscale + (g % S::kScales) * 2 * KT + 2 * (lane & 3);
-          const uint4* rows = smask + q * 128 + 32 * (warp & 3) + (lane >> 2);
-          if (masked) {  // what each row sees of this tile, by the thread that has it
-            uint32_t w[4];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) w[y] = y < KT / 32 ? mask.template word<KT>(base, y) : 0u;
-            __syncwarp();
-            smask[q * 128 + row] = make_uint4(w[0], w[1], w[2], w[3]);
-            __syncwarp();
-          }
-          uint32_t r[2][16];  // 32 columns of rows lane / 4 + 0, 8 and + 16, 24
-          // scores of part c: times the keys' scales, -infinity where the row does not see
-          auto load = [&](int c) {
-            tmem_ld_frag(ts + 32 * c, r[0]);
-            tmem_ld_frag(ts + (16u << 16) + 32 * c, r[1]);
-            float2 f[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f[j] = *(const float2*)(kscale + 32 * c + 8 * j);
-            tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                mul2(r[x >> 1][4 * j + 2 * (x & 1)], r[x >> 1][4 * j + 2 * (x & 1) + 1], f[j].x,
-                     f[j].y);
-            if (masked) {
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const uint32_t see = ((const uint32_t*)(rows + 8 * x))[c] >> (2 * (lane & 3));
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                  for (int e = 0; e < 2; ++e) {
-                    uint32_t& z = r[x >> 1][4 * j + 2 * (x & 1) + e];
-                    z = (see >> (8 * j + e)) & 1u ? z : 0xff800000u;
-                  }
-              }
-            }
-          };
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-          for (int c = 0; c < KT / 32; ++c) {
-            load(c);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                top[x] = fmaxf(fmaxf(top[x], __uint_as_float(r[x >> 1][4 * j + 2 * (x & 1)])),
-                               __uint_as_float(r[x >> 1][4 * j + 2 * (x & 1) + 1]));
-          }
-          bool grows = false;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
-            top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2)) * sl2;
-            grows |= top[x] > m4[x] + kRescale;
-          }
-          if (k == 0) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) m4[x] = top[x];
-          } else if (__any_sync(0xffffffffu, grows)) {
-            float mine4 = 1.f;  // the factor of this thread's row in TMEM
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float now = fmaxf(m4[x], top[x]);
-              const float keep = m4[x] == now ? 1.f : ex2(m4[x] - now);
-              l4[x] *= keep;
-              m4[x] = now;
-              const float v = __shfl_sync(0xffffffffu, keep, 4 * (lane & 7));
-              if (lane >> 3 == x) mine4 = v;
-            }
-            rescale(mine4);
-          }
-          float less[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) less[x] = m4[x] == -INFINITY ? 0.f : -m4[x];
-#pragma unroll 1
-          for (int c = 0; c < KT / 32; ++c) {
-            load(c);
-            float2 f[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f[j] = *(const float2*)(kscale + KT + 32 * c + 8 * j);
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              uint32_t pk[8];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                  const int x = 2 * t + z;
-                  float p0, p1;
-                  fma2(r[t][4 * j + 2 * z], r[t][4 * j + 2 * z + 1], sl2, less[x], p0, p1);
-                  p0 = ex2(p0);
-                  p1 = ex2(p1);
-                  l4[x] += p0 + p1;
-                  uint32_t w0 = __float_as_uint(p0), w1 = __float_as_uint(p1);
-                  mul2(w0, w1, f[j].x, f[j].y);
-                  pk[2 * j + z] = pack2(__uint_as_float(w0), __uint_as_float(w1));
-                }
-              }
-              tmem_st_frag16(ts + (t ? 16u << 16 : 0u) + 16 * c, pk);
-            }
-          }
         }
         tmem_wait_st();
         tc_fence_before();
@@ -889,17 +784,6 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
       if (q_started) finish_q();
       __syncwarp();
       if (lane == 0) free_item(n);  // (what is left of it is in registers)
-      if constexpr (!S::kTma) {
-        // statistics of this thread's row
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          l4[x] += __shfl_xor_sync(0xffffffffu, l4[x], 1);
-          l4[x] += __shfl_xor_sync(0xffffffffu, l4[x], 2);
-          const float mv = __shfl_sync(0xffffffffu, m4[x], 4 * (lane & 7));
-          const float lv = __shfl_sync(0xffffffffu, l4[x], 4 * (lane & 7));
-          if (lane >> 3 == x) m = mv, l = lv;
-        }
-      }
       ok = __all_sync(0xffffffffu, wait(&o_full[q], n_item & 1));
       if (!ok) break;
       ++n_item;
