@@ -227,7 +227,14 @@ struct TcShape {
   static constexpr int kThreads = kSoft + kMma + kLoad;
   static constexpr int kItems = 4;  // row tiles that the schedule is ahead
   static constexpr int kPerSm = NQ == 2 ? 1 : 2;
-  static constexpr uint32_t kTmemCols = NQ == 2 ? 512 : 256;  // S: 128 columns a row tile, O: D
+  // TMEM columns: S at 128 q, O at 128 NQ + D q, P where neither is.  Only for D = 128 with
+  // tiles of 128 keys is there no room left: P then lies over the upper half of S.  The next S
+  // follows the product that reads P in the pipe, with the same shape, and reaches these columns
+  // last.
+  static constexpr uint32_t kTmemCols = NQ == 2 ? 512 : 256;
+  static constexpr uint32_t p_at(uint32_t q) {
+    return D == 128 && KT == 128 ? 128 * q + 64 : NQ == 2 ? 384 + 64 * q : KT == 64 ? 64 : 192;
+  }
   static constexpr int kRows = 128 * NQ;
   static constexpr int kBars = 4 * kStages + 4 * NQ + kScales + 2 * kCodes + 2 * kItems;
   static constexpr size_t kCoded =
@@ -382,7 +389,7 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
               if (!ok) break;
 #pragma unroll
               for (int s = 0; s < KT / 16; ++s)
-                mma_ts(one, tmem + NQ * 128 + q * D, tmem + q * 128 + 8 * s, va + 128 * s, io,
+                mma_ts(one, tmem + NQ * 128 + q * D, tmem + S::p_at(q) + 8 * s, va + 128 * s, io,
                        !first || s != 0);
               // (between tiles s_full of the next one says it: it tracks all products so far)
               if (!sc || first_next) commit_if(one, &o_full[q]);
@@ -466,9 +473,9 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
               } else {
                 const int x = 2 * g + part, st = x % S::kCodes;
                 float* scales = sscale + (g % S::kScales) * 2 * KT;
-                // The scales' place was last used by tile g - 4.  The ring's (w_empty) was
-                // emptied by half x - 4, and before its codes were turned the one before it,
-                // which had waited for the keys' or values' place: P of tile g - 4 was there.
+                // The scales' place was last used by tile g - 4.  w_empty says that the keys
+                // of tile g - 2 were turned; before them the values of tile g - 3, which had
+                // waited for the product with those of tile g - 4: its softmax is done.
                 ok = __all_sync(0xffffffffu, wait(&w_empty[st], ((x / S::kCodes) & 1) ^ 1));
                 if (!ok) break;
                 if (base < 0) {  // the tree's rows come as bf16, without scales
@@ -540,8 +547,6 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
 #pragma unroll
             for (int i = 0; i < kPieces; ++i)
               w[i] = *(const uint4*)(scode + st * S::kCodeBytes + from + i * kStep * D);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&w_empty[st]);
             ok = __all_sync(0xffffffffu, wait(part ? v_empty : k_empty, (g & 1) ^ 1));
             if (!ok) break;
             if (base >= 0) {
@@ -573,6 +578,10 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
             fence_async_smem();
             mbar_arrive(part ? v_full : k_full);
             if (part == 0) mbar_arrive(&c_full[g % S::kScales]);
+            // The codes' place is free only now: told so before the wait for the operand's
+            // place, the next copy could arrive before the loads above had been carried out.
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&w_empty[st]);
           }
         }
         __syncwarp();
@@ -585,6 +594,7 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
     const int q = warp >> 2, row = tid & 127;
     const uint32_t quad = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + quad + q * 128, to = tmem + quad + NQ * 128 + q * D;
+    const uint32_t tp = tmem + quad + S::p_at(q);
     uint8_t* my_q = sq + q * S::kQTile;
     const float sl2 = a.scale * kL2e;
     // item n's queries into shared memory, zeros where there is no row
@@ -727,10 +737,11 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
             rescale(keep);
           }
           const float less = m == -INFINITY ? 0.f : -m;
-          // ---- weights, in bf16 for the second product, over the scores
+          // ---- weights, in bf16 for the second product
           float la[4] = {0.f, 0.f, 0.f, 0.f};
+          // (from the last part on: P's parts lie over parts of S that were read already)
 #pragma unroll (kKeep == 1 ? 1 : kParts)
-          for (int w = 0; w < kParts; ++w) {
+          for (int w = kParts - 1; w >= 0; --w) {
             if (kKeep == 1) load(w);
             uint32_t pk[16];
 #pragma unroll
@@ -756,7 +767,7 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
               pk[e / 2] = pack2(p[0], p[1]);
               pk[e / 2 + 1] = pack2(p[2], p[3]);
             }
-            tmem_st16(ts + 16 * w, pk);
+            tmem_st16(tp + 16 * w, pk);
           }
           l += (la[0] + la[1]) + (la[2] + la[3]);
         }

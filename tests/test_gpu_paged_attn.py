@@ -410,3 +410,213 @@ def test_bad_pages_read_as_zeros(rows, code):
         v[32:48] = 0
         o, mag, big = oracle.chunk(q64, k, v, 100, 0, 0, 0.125)
         assert np.all(np.abs(values(out) - o) <= _bound(o, mag, big, 64, 100, "bf16"))
+
+
+@pytest.mark.parametrize("code", ["bf16", "e4m3", "i8"])
+@pytest.mark.parametrize("d,batch,rows", [(128, 40, 16), (64, 50, 32), (128, 9, 200), (128, 60, 1)])
+def test_many_tiles_on_every_sm_give_the_same_bits_and_are_right(code, d, batch, rows):
+    """Every SM has several row tiles and hundreds of key tiles: what loads, converts, multiplies
+    and sums runs at its own pace.  Repeats are equal, and a few requests are checked."""
+    g = np.random.default_rng(batch)
+    lens = [int(x) for x in g.integers(max(rows, 500), 3000, batch)]
+    pool = Pool(g, lens, 64, 8, d, code)
+    q, q64 = _q(g, (batch * rows, 32, d), "bf16")
+    start, kv = cuda(np.arange(batch + 1, dtype=np.int32) * rows), cuda(np.array(lens, np.int32))
+    table, ws = cuda(pool.table), dt.workspace(dt.paged_attn_workspace_bytes(batch, batch * rows, 32, 8, d))
+    outs = []
+    for _ in range(8):
+        out = torch.zeros_like(q)
+        dt.paged_attn(q, start, pool.cache, table, kv, d ** -0.5, out, ws, max_rows=rows)
+        outs.append(out)
+    assert dt.read_status(ws) == 0
+    assert all(torch.equal(outs[0], o) for o in outs[1:])
+    got = values(outs[0])
+    for b in g.integers(0, batch, 4):
+        k, v = pool.rows(b, lens[b])
+        pick = np.unique([0, rows // 2, rows - 1])
+        ok = np.stack([oracle.seen_positions(lens[b] - rows + i, lens[b], 0, 0) for i in pick])
+        o, mag, big = oracle.attend(q64[b * rows + pick], k, v, ok, d ** -0.5)
+        err = np.abs(got[b * rows + pick] - o)
+        assert np.all(err <= _bound(o, mag, big, d, lens[b], "bf16"))
+
+
+# -------------------------------------------------- values nobody may see --
+def _spoil(pool, b, j, page, value, code):
+    """Position j of request b holds ``value`` in V (or, in a quantised cache, a scale of NaN)."""
+    p, s = int(pool.table[b, j // page]), j % page
+    if code == "bf16":
+        pool.cache.v[p, :, s] = value
+        pool.cache.k[p, :, s] = value
+    else:
+        pool.cache.v_scale[p, :, s] = float("nan")
+        pool.cache.k_scale[p, :, s] = float("nan")
+
+
+@pytest.mark.parametrize("code", ["bf16", "e4m3", "i8"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("n,lens", [(40, [300]), (5, [130]), (200, [1500]), (2, [9000])])
+def test_a_position_that_is_not_a_number_reaches_only_the_rows_that_see_it(code, value, n, lens):
+    """One late position of the chunk is spoilt: the rows before it share its tile with rows that
+    see it, and their weight for it is 0.  They must be as if it were not there."""
+    g = np.random.default_rng(n)
+    page, L = 32, lens[0]
+    pool = Pool(g, lens, page, 2, 64, code)
+    k, v = pool.rows(0, L)
+    first = L - n + n // 2                    # row n // 2 and later see the spoilt position
+    _spoil(pool, 0, first, page, value, code)
+    q, q64 = _q(g, (n, 8, 64), "bf16")
+    out = torch.zeros_like(q)
+    ws = dt.workspace(dt.paged_attn_workspace_bytes(1, n, 8, 2, 64))
+    dt.paged_attn(q, cuda(np.array([0, n], np.int32)), pool.cache, cuda(pool.table),
+                  cuda(np.array(lens, np.int32)), 0.125, out, ws, max_rows=n)
+    assert dt.read_status(ws) == 0
+    got = values(out)
+    o, mag, big = oracle.chunk(q64, k, v, L, 0, 0, 0.125)
+    clean = slice(0, n // 2)
+    assert np.all(np.abs(got[clean] - o[clean]) <= _bound(o, mag, big, 64, L, "bf16")[clean])
+    assert not np.any(np.isfinite(got[n // 2 :]).all(-1))
+
+
+@pytest.mark.parametrize("code", ["bf16", "i8"])
+def test_a_spoilt_position_behind_the_window(code):
+    g = np.random.default_rng(3)
+    L, n, page, window = 700, 70, 16, 100
+    pool = Pool(g, [L], page, 2, 128, code)
+    k, v = pool.rows(0, L)
+    j = L - n - window + 30                   # rows 0 .. 29 see it, later ones do not
+    _spoil(pool, 0, j, page, float("nan"), code)
+    q, q64 = _q(g, (n, 4, 128), "bf16")
+    out = torch.zeros_like(q)
+    ws = dt.workspace(dt.paged_attn_workspace_bytes(1, n, 4, 2, 128))
+    dt.paged_attn(q, cuda(np.array([0, n], np.int32)), pool.cache, cuda(pool.table),
+                  cuda(np.array([L], np.int32)), 0.1, out, ws, max_rows=n, window=window)
+    o, mag, big = oracle.chunk(q64, k, v, L, window, 0, 0.1)
+    got, seen = values(out), np.array([oracle.seen_positions(L - n + i, L, window, 0)[j] for i in range(n)])
+    assert seen[0] and not seen[-1]
+    tol = _bound(o, mag, big, 128, L, "bf16")
+    assert np.all(np.abs(got - o)[~seen] <= tol[~seen])
+    assert not np.any(np.isfinite(got[seen]).all(-1))
+
+
+@pytest.mark.parametrize("code", ["bf16", "e4m3"])
+def test_a_tree_row_that_is_not_a_number_reaches_only_its_descendants(code):
+    g = np.random.default_rng(4)
+    L, nmax = 200, 12
+    pool = Pool(g, [L], 32, 2, 64, code)
+    _, depth, anc = random_tree(g, nmax)
+    depth, anc = depth[None], anc[None]
+    q, q64 = _q(g, (1, nmax + 1, 8, 64), "bf16")
+    kt, kt64 = _q(g, (1, nmax + 1, 2, 64), "bf16")
+    vt, vt64 = _q(g, (1, nmax + 1, 2, 64), "bf16")
+    bad = 4                                   # node 4 = tree row 5
+    vt[0, bad + 1] = float("nan")
+    out = torch.zeros_like(q)
+    ws = dt.workspace(dt.verify_paged_workspace_bytes(1, nmax, 8, 2, 64))
+    dt.tree_verify_attn_paged(q, pool.cache, cuda(pool.table), cuda(np.array([L], np.int32)), kt, vt,
+                              cuda(anc.view(np.int64)), cuda(np.array([nmax], np.int32)), 0.125, out, ws)
+    k, v = pool.rows(0, L)
+    o, mag, big = oracle.tree(q64[0], k, v, kt64[0], vt64[0], anc[0], depth[0], nmax, L, 0, 0, 0.125)
+    got = values(out)[0]
+    below = np.array([False] + [bool((int(a) >> bad) & 1) for a in anc[0]])
+    tol = _bound(o, mag, big, 64, L + nmax + 1, "bf16")
+    assert np.all(np.abs(got - o)[~below] <= tol[~below])
+    assert below.sum() >= 1 and not np.any(np.isfinite(got[below]).all(-1))
+
+
+# ------------------------------------------------------------ every code --
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("code", ["e4m3", "i8"])
+def test_every_code_is_read_exactly(code, n):
+    """Value column e of position j holds code (j + e) % 256; a query of zeros weighs all positions
+    alike, so each output is a mean of known codes: only its own rounding, and that of the equal
+    weights (times the one scale, a power of two: exact), is left."""
+    L, page, d = 256, 64, 64
+    codes = (np.arange(L)[:, None] + np.arange(d)[None]) % 256
+    raw = codes.astype(np.uint8)
+    if code == "e4m3":
+        raw = np.where((raw & 0x7F) == 0x7F, raw & 0x80, raw)   # no NaN codes: dt_kv_write makes none
+    t = torch.as_tensor(raw).view(DTYPES[code])
+    val = t.float().double().numpy()
+    cache = dt.KVCache.empty(L // page, page, 1, d, DTYPES[code])
+    cache.v.view(torch.uint8).copy_(torch.as_tensor(raw).view(L // page, 1, page, d))
+    cache.v_scale.fill_(0.25)
+    cache.k_scale.fill_(1.0)
+    q = torch.zeros(n, 2, d, dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros_like(q)
+    ws = dt.workspace(dt.paged_attn_workspace_bytes(1, n, 2, 1, d))
+    table = cuda(np.arange(L // page, dtype=np.int32)[None])
+    dt.paged_attn(q, cuda(np.array([0, n], np.int32)), cache, table, cuda(np.array([L], np.int32)), 0.1, out,
+                  ws, max_rows=n)
+    got = values(out)
+    for i in range(n):
+        seen = val[: L - n + i + 1] * 0.25
+        o, mag = seen.mean(0), np.abs(seen).mean(0)
+        assert np.all(np.abs(got[i] - o) <= 2.0 ** -8 * np.abs(o) + (L + 2) * 2.0 ** -24 * mag)
+
+
+@pytest.mark.parametrize("rows", [1, 33])
+@pytest.mark.parametrize("code", ["bf16", "i8"])
+def test_a_cache_of_more_than_four_gigabytes(code, rows):
+    """Pages at the far end of a large pool: offsets pass 32 bits."""
+    g = np.random.default_rng(rows)
+    page, hkv, d = 64, 2, 128
+    pages = (5 << 30) // (page * hkv * d * (2 if code == "bf16" else 1))
+    free = torch.cuda.mem_get_info()[0]
+    assert free > 14 << 30
+    small = Pool(g, [150], page, hkv, d, code)
+    used = small.cache.k.shape[0]
+    new = lambda t: None if t is None else torch.zeros(pages, *t.shape[1:], dtype=t.dtype, device="cuda")
+    big = dt.KVCache(*(new(t) for t in (small.cache.k, small.cache.v, small.cache.k_scale,
+                                        small.cache.v_scale)))
+    for a, b in ((big.k, small.cache.k), (big.v, small.cache.v), (big.k_scale, small.cache.k_scale),
+                 (big.v_scale, small.cache.v_scale)):
+        if b is not None:
+            a[pages - used :] = b
+    q, q64 = _q(g, (rows, 8, d), "bf16")
+    out = torch.zeros_like(q)
+    ws = dt.workspace(dt.paged_attn_workspace_bytes(1, rows, 8, hkv, d))
+    dt.paged_attn(q, cuda(np.array([0, rows], np.int32)), big, cuda(small.table + (pages - used)),
+                  cuda(np.array([150], np.int32)), 0.1, out, ws, max_rows=rows)
+    assert dt.read_status(ws) == 0
+    k, v = small.rows(0, 150)
+    o, mag, bigs = oracle.chunk(q64, k, v, 150, 0, 0, 0.1)
+    assert np.all(np.abs(values(out) - o) <= _bound(o, mag, bigs, d, 150, "bf16"))
+
+
+# ----------------------------------------------------- batches and shares --
+@pytest.mark.parametrize("code,rows", [("bf16", 1), ("e4m3", 1), ("i8", 9), ("bf16", 40)])
+def test_many_requests_of_very_different_lengths(code, rows):
+    """More requests than a warp has lanes, some without rows, most of them short."""
+    g = np.random.default_rng(11)
+    lens = [int(x) for x in g.integers(1, 60, 150)] + [3000, 1, 700]
+    n = [0 if i % 7 == 3 else min(x, rows) for i, x in enumerate(lens)]
+    _chunk(g, lens, n, 16, 4, 2, 64, code, "bf16", max_rows=rows)
+
+
+@pytest.mark.parametrize("hq,hkv", [(16, 1), (12, 1), (40, 2), (300, 1)])
+@pytest.mark.parametrize("rows", [1, 2])
+def test_group_sizes_at_the_kernels_borders(hq, hkv, rows):
+    """8, 16 and 128 (row, head) pairs are where the kernels' tiles end."""
+    _chunk(np.random.default_rng(hq), [200, 33], [rows, 1], 16, hq, hkv, 64, "i8", "bf16")
+
+
+def test_a_window_over_shares_that_see_different_tiles():
+    """First tokens, then a window far behind them, cut over many CTAs."""
+    _chunk(np.random.default_rng(2), [20000], [3], 64, 32, 1, 128, "bf16", "bf16", 5000, 300)
+    _chunk(np.random.default_rng(2), [9000], [150], 128, 4, 1, 64, "e4m3", "bf16", 3000, 200)
+
+
+def test_another_device_s_workspace_and_cpu_tensors_are_refused():
+    pool = Pool(np.random.default_rng(0), [20], 16, 2, 64, "bf16")
+    q, _ = _q(np.random.default_rng(0), (1, 4, 64), "bf16")
+    ws = dt.workspace(dt.paged_attn_workspace_bytes(1, 1, 4, 2, 64))
+    start, table, kv = cuda(np.array([0, 1], np.int32)), cuda(pool.table), cuda(np.array([20], np.int32))
+    call = lambda **kw: dt.paged_attn(*[{**dict(q=q, s=start, c=pool.cache, t=table, k=kv, x=0.1,
+                                               o=torch.zeros_like(q), w=ws), **kw}[n] for n in "qsctkxow"],
+                                      max_rows=1)
+    call()
+    for kw in (dict(w=ws.cpu()), dict(t=table.cpu()), dict(k=kv.cpu()), dict(q=q.cpu()), dict(o=q.cpu())):
+        with pytest.raises(ValueError):
+            call(**kw)
+    with pytest.raises(dt.DtreeError):
+        call(w=ws[:1024])
