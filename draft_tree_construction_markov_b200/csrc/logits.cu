@@ -17,6 +17,10 @@
 //
 // Bound: memory, each live row read and written once; the history is re-read
 // by every slice of its request, from L2.
+// Measured (B200): 16 trees of up to 32 nodes, V = 151936, bf16, histories of 256
+// to 8192 tokens, 64 biases and a mask a node: 213 MB in 83 us (2.6 TB/s).  What
+// is left over the copy is each CTA's table (counted anew for every slice and
+// group of rows) and the last CTAs of the largest trees.
 #include <limits.h>
 
 #include "common.cuh"

@@ -20,6 +20,13 @@
 // g (g even) or g ^ 4 (g odd) of the piece, which keeps the 16-byte reads of
 // both products free of bank conflicts in the swizzled ring.
 // P^T is S^T's fragment transposed (movmatrix).
+//
+// Measured (B200): 64 single tokens over 512 to 65536 positions, 32 / 8 heads of
+// 128, e4m3 cache: 372 MB in 110 us with the join, 3.4 TB/s (0.52 of the measured
+// copy rate).  What holds it up is the conversion: five integer instructions, at
+// two cycles each, for four codes (eight with neighbours paired).  Fifteen
+// workers of 16-position pieces instead of eleven of 32: 179 us, since the
+// loader's work is per piece.
 #include <algorithm>
 
 #include "paged_attn.cuh"

@@ -13,17 +13,31 @@
 // by the sum undoes exactly, so most key tiles touch O in the tensor core only.
 //
 // Roles: NQ softmax warpgroups, each with a row tile of its own that shares the
-// keys and values in shared memory; one thread that issues the MMAs; and the
-// loaders.  A bf16 cache comes by TMA, a page (or 128 rows of it) a box; an
-// 8-bit cache is read with 16-byte loads a tile ahead, turned into bf16 (exact
-// for every code, see codes_to_bf16) and stored swizzled by a warpgroup, with
-// the row scales beside it: those of K multiply S, those of V multiply P.
+// keys and values in shared memory; a warp that issues the MMAs; one that walks
+// the list of work for all others; and one that issues the copies.  A bf16 cache
+// comes by TMA straight into the operands, a page (or 128 rows of it) a box.
+// Codes of an 8-bit cache come the same way into a ring, with the scales of
+// their rows; a warpgroup turns them into bf16 (exact for every code, see
+// codes_to_bf16).  The scales of K multiply S, those of V multiply P, in fp32.
 // While one row tile's softmax runs, the tensor core works for the other (NQ =
-// 2), or for the second CTA of the SM (NQ = 1).
+// 2, for more than 128 (row, head) pairs), or for the second CTA of the SM.
 //
 // The work of a call (row tiles x KV heads x key tiles) is divided over the
 // CTAs in equal consecutive shares; a row tile that two shares cut is joined by
 // paged_join_kernel from fp32 partials.
+//
+// Bound and measured (B200): three chunks of up to 2048 rows over up to 8192
+// positions, 32 / 8 heads of 128, bf16 cache: 479 GFLOP in 0.55 ms, 875 TFLOP/s
+// (0.53 of the measured peak).  2 x 128 x 128 exponentials a key tile take the
+// SM's special-function units as long (2048 cycles) as its products the tensor
+// core; a tile takes about 3600, the rest being the two softmaxes' other
+// instructions and the wait between a softmax and the products it feeds.  The
+// same over int8 with a 4096-position window: 450 GFLOP in 0.85 ms.  There the
+// reads of the scales (96 wide shared loads a row and tile, which all lanes
+// repeat) and the conversion hold the softmax up; other forms were measured
+// and are no faster: scores in fragment layout, where a lane needs a quarter of
+// the scales but TMEM gives the same data in 74 instead of 27 cycles, 0.84 ms;
+// key tiles of 64 with all scores in registers, 1.04 ms.
 #include <algorithm>
 #include <type_traits>
 
@@ -793,8 +807,6 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
       }
       if (!ok) break;
       if (q_started) finish_q();
-      __syncwarp();
-      if (lane == 0) free_item(n);  // (what is left of it is in registers)
       ok = __all_sync(0xffffffffu, wait(&o_full[q], n_item & 1));
       if (!ok) break;
       ++n_item;
@@ -840,6 +852,8 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
         }
       }
       tc_fence_before();
+      __syncwarp();
+      if (lane == 0) free_item(n);
     }
   }
   __syncwarp();

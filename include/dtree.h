@@ -517,8 +517,11 @@ dt_status dt_kv_read(const dt_kv_cache* cache, const int32_t* d_page_table, int 
  *   max_rows  no request has more rows; it decides how the work is split
  *   window >= 0 (0: no window), n_sink >= 0 (ignored without a window)
  * Rows outside every request's range are left as they were.  Scores, softmax
- * statistics and sums are fp32; the softmax weights enter the second product
- * as bf16 (dt = DT_BF16).  A request longer than its page table's row, with
+ * statistics and sums are fp32; the softmax weights (times the value's scale,
+ * in a scaled cache) enter the second product as bf16 (dt = DT_BF16).  A value
+ * that is infinite or NaN at a position reaches the rows that see the position
+ * and no others.  The DT_E4M3 codes 0x7f and 0xff (not a number; dt_kv_write
+ * makes none) count as +-480 with dt = DT_BF16.  A request longer than its page table's row, with
  * more than max_rows rows, or with a negative length records DT_EDEVICE and
  * its rows are left as they were. */
 size_t dt_paged_attn_workspace_bytes(int batch, int total_rows, int Hq, int Hkv, int d);
