@@ -551,7 +551,8 @@ cudaError_t launch_paged_decode(const PagedArgs& a, int ct, const dt_kv_cache* c
       !paged_map(&maps.v, cache->d_v, bytes, a.d, slots, box))
     return cudaErrorInvalidValue;
   const int ctas = std::min(dt_num_sms(), kPagedSms);
-  // a request that can have a few pieces at most is not worth a join
+  // requests of at most a few pieces are not cut, which saves the join (one token over 33
+  // positions: 10 us against 13 us)
   const int shift = (int64_t)a.c.max_pages << a.c.page_shift <= 128 ? 30 : 5;
 #define DT_DECODE(DD, CC)                                                 \
   if (a.d == DD && ct == CC)                                              \
