@@ -15,6 +15,13 @@ namespace dt {
 // Every workspace starts with a 256-byte header; word 0 is the status word.
 constexpr size_t kWsHeader = 256;
 
+// A workspace of at least `need` bytes, on 16 bytes: behind the header lie
+// records that kernels read and write as vectors.
+inline dt_status check_ws(const void* ws, size_t bytes, size_t need) {
+  if (!ws || bytes < need) return DT_EWORKSPACE;
+  return (uintptr_t)ws & 15 ? DT_EINVAL : DT_OK;
+}
+
 __device__ __forceinline__ void set_status(int32_t* status, int32_t code) {
   if (status) atomicCAS(status, 0, code);
 }

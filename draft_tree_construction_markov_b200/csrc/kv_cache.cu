@@ -313,14 +313,14 @@ dt_status dt_kv_write(const void* d_k, const void* d_v, int64_t ld_k, int64_t ld
                       const int32_t* d_row_start, const int32_t* d_pos,
                       const int32_t* d_page_table, int max_pages, int batch, int total_rows,
                       const dt_kv_cache* cache, void* ws, size_t ws_bytes, dt_stream stream) {
-  const dt_status ok = check_cache(cache, d_page_table, max_pages, batch);
+  dt_status ok = check_cache(cache, d_page_table, max_pages, batch);
   if (ok != DT_OK) return ok;
   if (!d_k || !d_v || !d_row_start || !d_pos || total_rows < 0) return DT_EINVAL;
   if (dt != DT_F32 && dt != DT_BF16) return DT_EINVAL;
   if (((uintptr_t)d_k | (uintptr_t)d_v) & (dt == DT_F32 ? 3 : 1)) return DT_EINVAL;
   const int64_t row = (int64_t)cache->Hkv * cache->d;
   if (ld_k < row || ld_v < row) return DT_EINVAL;
-  if (!ws || ws_bytes < kWsHeader) return DT_EWORKSPACE;
+  if ((ok = check_ws(ws, ws_bytes, kWsHeader)) != DT_OK) return ok;
   WriteArgs a = {};
   a.k = d_k;
   a.v = d_v;
@@ -341,14 +341,14 @@ dt_status dt_kv_commit(const void* d_k_tree, const void* d_v_tree, dt_dtype dt,
                        const int32_t* d_pos, const int32_t* d_page_table, int max_pages,
                        int batch, const dt_kv_cache* cache, void* ws, size_t ws_bytes,
                        dt_stream stream) {
-  const dt_status ok = check_cache(cache, d_page_table, max_pages, batch);
+  dt_status ok = check_cache(cache, d_page_table, max_pages, batch);
   if (ok != DT_OK) return ok;
   if (!d_k_tree || !d_v_tree || !d_acc_nodes || !d_n_acc || !d_pos) return DT_EINVAL;
   if (dt != DT_F32 && dt != DT_BF16) return DT_EINVAL;
   if (((uintptr_t)d_k_tree | (uintptr_t)d_v_tree) & (dt == DT_F32 ? 3 : 1)) return DT_EINVAL;
   if (Bk < 1 || Nmax < 1) return DT_EINVAL;
   if (Bk > 64 || Nmax > 64) return DT_EUNSUPPORTED;
-  if (!ws || ws_bytes < kWsHeader) return DT_EWORKSPACE;
+  if ((ok = check_ws(ws, ws_bytes, kWsHeader)) != DT_OK) return ok;
   WriteArgs a = {};
   a.k = d_k_tree;
   a.v = d_v_tree;
@@ -369,12 +369,12 @@ dt_status dt_kv_read(const dt_kv_cache* cache, const int32_t* d_page_table, int 
                      const int32_t* d_row_start, const int32_t* d_pos, int batch, int total_rows,
                      dt_dtype dt, void* d_k_out, void* d_v_out, void* ws, size_t ws_bytes,
                      dt_stream stream) {
-  const dt_status ok = check_cache(cache, d_page_table, max_pages, batch);
+  dt_status ok = check_cache(cache, d_page_table, max_pages, batch);
   if (ok != DT_OK) return ok;
   if (!d_row_start || !d_pos || !d_k_out || !d_v_out || total_rows < 0) return DT_EINVAL;
   if (dt != DT_F32 && dt != DT_BF16) return DT_EINVAL;
   if (((uintptr_t)d_k_out | (uintptr_t)d_v_out) & 15) return DT_EINVAL;
-  if (!ws || ws_bytes < kWsHeader) return DT_EWORKSPACE;
+  if ((ok = check_ws(ws, ws_bytes, kWsHeader)) != DT_OK) return ok;
   const int64_t blocks = ((int64_t)total_rows + kKvThreads / 32 - 1) / (kKvThreads / 32);
   if (total_rows == 0) return DT_OK;
   ReadArgs a;

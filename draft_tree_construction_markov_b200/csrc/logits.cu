@@ -345,7 +345,8 @@ dt_status dt_logits_process(const void* d_logits, dt_dtype dt, const int32_t* d_
   const size_t bytes = (size_t)batch * (Nmax + 1) * V * (dt == DT_BF16 ? 2 : 4);
   const uintptr_t x = (uintptr_t)d_logits, y = (uintptr_t)d_out;
   if (x != y && x < y + bytes && y < x + bytes) return DT_EINVAL;  // partial overlap
-  if (!ws || ws_bytes < kWsHeader) return DT_EWORKSPACE;
+  const dt_status ok = check_ws(ws, ws_bytes, kWsHeader);
+  if (ok != DT_OK) return ok;
   LogitsArgs a;
   a.in = d_logits;
   a.out = d_out;

@@ -326,8 +326,8 @@ dt_status dt_paged_attn(const void* d_q, int64_t ld_q, const int32_t* d_row_star
   if (!d_row_start || !d_kv_len || total_rows < 0 || max_rows < 1) return DT_EINVAL;
   if (ld_q < (int64_t)Hq * cache->d || (ld_q * (dt == DT_F32 ? 4 : 2)) % 16) return DT_EINVAL;
   if ((int64_t)total_rows * Hq >= (int64_t)1 << 30) return DT_EUNSUPPORTED;
-  if (!ws || ws_bytes < paged_workspace((int64_t)total_rows * (Hq / cache->Hkv), cache->d))
-    return DT_EWORKSPACE;
+  ok = check_ws(ws, ws_bytes, paged_workspace((int64_t)total_rows * (Hq / cache->Hkv), cache->d));
+  if (ok != DT_OK) return ok;
   PagedArgs a = {};
   a.q = d_q;
   a.ld_q = ld_q;
@@ -372,7 +372,8 @@ dt_status dt_tree_verify_attn_paged(const void* d_q, const dt_kv_cache* cache,
   if (Nmax > 64 || (window && window <= Nmax)) return DT_EUNSUPPORTED;
   const int rows = batch * (Nmax + 1);
   if ((int64_t)rows * Hq >= (int64_t)1 << 30) return DT_EUNSUPPORTED;
-  if (!ws || ws_bytes < paged_workspace((int64_t)(Nmax + 1) * (Hq / cache->Hkv), cache->d)) return DT_EWORKSPACE;
+  ok = check_ws(ws, ws_bytes, paged_workspace((int64_t)(Nmax + 1) * (Hq / cache->Hkv), cache->d));
+  if (ok != DT_OK) return ok;
   PagedArgs a = {};
   a.q = d_q;
   a.ld_q = (int64_t)Hq * cache->d;

@@ -447,7 +447,8 @@ dt_status dt_calib_fit(const int32_t* d_depth, const float* d_ell, const int8_t*
  *            Hkv * page_size < 2^31, max_pages * page_size < 2^30,
  *            total_rows * Hq < 2^30
  *   base pointers of K, V and the cache arrays 16-byte aligned
- *   ws       its first 256 bytes cleared before the first use.  These calls
+ *   ws       16-byte aligned (else DT_EINVAL; dt_logits_process too), its
+ *            first 256 bytes cleared before the first use.  These calls
  *            leave the status word as it is unless they record an error, so
  *            dt_read_status() reports (and clears) the first of any number
  *            of calls.
