@@ -335,13 +335,15 @@ class KVCache:
     """A paged pool of keys and values (dt_kv_cache in the C header).
 
     ``k``, ``v``: [n_pages, Hkv, page_size, d], bfloat16, float32, float8_e4m3fn or int8;
-    ``k_scale``, ``v_scale``: [n_pages, Hkv, page_size] float32 for the 8-bit types, else None."""
+    ``k_scale``, ``v_scale``: [n_pages, Hkv, page_size] float32 for the 8-bit types, else None.
+    The tensors are the caller's to fill, but not to exchange: the attributes cannot be set (a larger
+    pool is another KVCache), and a call on tensors whose storage has moved raises."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         code = _lib.cache_dtype_code(k)
         if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype:
             raise ValueError("KVCache: k and v must be [n_pages, Hkv, page_size, d] of one type")
-        self.device = dev = k.get_device()
+        dev = k.get_device()
         scaled = code in (_lib.DT_E4M3, _lib.DT_I8)
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             if scaled != (t is not None):
@@ -349,10 +351,14 @@ class KVCache:
         at = [_arg("KVCache", name, t, dev, k.dtype, *k.shape) for name, t in (("k", k), ("v", v))]
         at += [_opt("KVCache", name, t, dev, _F32, *k.shape[:3])
                for name, t in (("k_scale", k_scale), ("v_scale", v_scale))]
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.n_pages, self.Hkv, self.page_size, self.d = k.shape
-        self._c = _lib.KvCacheStruct(*at, self.n_pages, self.page_size, self.Hkv, self.d, code)
-        self._ref = ctypes.byref(self._c)
+        n_pages, Hkv, page_size, d = k.shape
+        c = _lib.KvCacheStruct(*at, n_pages, page_size, Hkv, d, code)
+        self.__dict__.update(
+            k=k, v=v, k_scale=k_scale, v_scale=v_scale, n_pages=n_pages, Hkv=Hkv, page_size=page_size, d=d,
+            device=dev, _c=c, _ref=ctypes.byref(c), _at=(k, v, k_scale, v_scale, *at))
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"KVCache: {name} cannot be set; make a new KVCache")
 
     @staticmethod
     def empty(n_pages, page_size, Hkv, d, dtype=torch.bfloat16, device="cuda"):
@@ -364,7 +370,11 @@ class KVCache:
 
 
 def _table(where, cache, t):
-    """Address and shape of a page table."""
+    """Address and shape of a page table; looks whether the cache is still where it was."""
+    k, v, ks, vs, at_k, at_v, at_ks, at_vs = cache._at
+    if (k.data_ptr() != at_k or v.data_ptr() != at_v
+            or ks is not None and (ks.data_ptr() != at_ks or vs.data_ptr() != at_vs)):
+        raise ValueError(f"{where}: the cache's tensors have moved; make a new KVCache")
     if t.dim() != 2:
         raise ValueError(f"{where}: page_table must be [batch, max_pages]")
     batch, pages = t.shape

@@ -19,3 +19,44 @@ def test_a_workspace_off_16_bytes_is_refused(call, at):
     """Behind its header lie records that are read and written 16 bytes at a time."""
     assert call(ws=ctypes.c_void_p(at)) == EINVAL
     assert call(ws=ctypes.c_void_p(at), bytes=8) == EWORKSPACE
+
+
+def _cpu_cache(dtype=torch.int8):
+    return dt.KVCache.empty(4, 16, 2, 64, dtype, device="cpu")
+
+
+@pytest.mark.parametrize("name", ["k", "v", "k_scale", "v_scale", "n_pages", "Hkv", "page_size", "d", "device"])
+def test_a_cache_s_attributes_cannot_be_set(name):
+    """The calls go by what the constructor saw: a larger pool assigned later would leave them on the
+    old one, which nothing keeps alive."""
+    c = _cpu_cache()
+    old = getattr(c, name)
+    with pytest.raises(AttributeError):
+        setattr(c, name, torch.zeros(8, 2, 16, 64, dtype=torch.int8))
+    assert getattr(c, name) is old
+    c.k[0].fill_(3)                                       # filling them is what they are for
+
+
+@pytest.mark.parametrize("dtype,part", [(torch.bfloat16, 0), (torch.bfloat16, 1), (torch.int8, 0), (torch.int8, 1),
+                                        (torch.int8, 2), (torch.int8, 3)])
+@pytest.mark.parametrize("grow", [False, True])
+def test_a_cache_whose_storage_has_moved_is_refused(dtype, part, grow):
+    c = _cpu_cache(dtype)
+    t = (c.k, c.v, c.k_scale, c.v_scale)[part]
+    if grow:
+        t.resize_(64, *t.shape[1:])
+    else:
+        t.data = torch.zeros_like(t)
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    ws = torch.zeros(256, dtype=torch.uint8)
+    x, q = torch.zeros(10, 2, 64), torch.zeros(10, 4, 64, dtype=torch.bfloat16)
+    tree, kt = torch.zeros(2, 9, 4, 64, dtype=torch.bfloat16), torch.zeros(2, 9, 2, 64, dtype=torch.bfloat16)
+    for call in (lambda: dt.kv_write(x, x, i(3), i(2), c, i(2, 4), ws),
+                 lambda: dt.kv_read(c, i(2, 4), i(3), i(2), x, x.clone(), ws),
+                 lambda: dt.kv_commit(kt, kt, i(2, 4), i(2), i(2), c, i(2, 4), ws),
+                 lambda: dt.paged_attn(q, i(3), c, i(2, 4), i(2), 0.1, q.clone(), ws, max_rows=5),
+                 lambda: dt.tree_verify_attn_paged(tree, c, i(2, 4), i(2), kt, kt,
+                                                   torch.zeros(2, 8, dtype=torch.int64), i(2), 0.1, tree.clone(),
+                                                   ws)):
+        with pytest.raises(ValueError, match="moved"):
+            call()
