@@ -264,6 +264,15 @@ dt_status run_paged(PagedArgs a, const dt_kv_cache* cache, int dt, void* ws, cud
   return e == cudaSuccess ? DT_OK : DT_ECUDA;
 }
 
+// Has [p, p + n) a byte in common with any of `rows` pieces of w bytes that lie ld bytes
+// apart from q on?  (A row that is done again reads its query once more after rows of the
+// output were written, and other CTAs read theirs at any time.)
+bool meets(const void* out, size_t n, const void* in, int64_t rows, size_t ld, size_t w) {
+  const uintptr_t p = (uintptr_t)out, q = (uintptr_t)in;
+  const int64_t i = p < q + w ? 0 : (int64_t)((p - q - w) / ld) + 1;  // first that ends behind p
+  return n && i < rows && q + i * ld < p + n;
+}
+
 // checks that both entry points share, after the cache's own
 dt_status check_paged(const dt_kv_cache* c, const void* q, const void* out, int Hq, float scale,
                       int window, int n_sink, dt_dtype dt) {
@@ -328,6 +337,8 @@ dt_status dt_paged_attn(const void* d_q, int64_t ld_q, const int32_t* d_row_star
   if ((int64_t)total_rows * Hq >= (int64_t)1 << 30) return DT_EUNSUPPORTED;
   ok = check_ws(ws, ws_bytes, paged_workspace((int64_t)total_rows * (Hq / cache->Hkv), cache->d));
   if (ok != DT_OK) return ok;
+  const size_t es = dt == DT_F32 ? 4 : 2, row = (size_t)Hq * cache->d * es;
+  if (meets(d_out, total_rows * row, d_q, total_rows, ld_q * es, row)) return DT_EINVAL;
   PagedArgs a = {};
   a.q = d_q;
   a.ld_q = ld_q;
@@ -374,6 +385,11 @@ dt_status dt_tree_verify_attn_paged(const void* d_q, const dt_kv_cache* cache,
   if ((int64_t)rows * Hq >= (int64_t)1 << 30) return DT_EUNSUPPORTED;
   ok = check_ws(ws, ws_bytes, paged_workspace((int64_t)(Nmax + 1) * (Hq / cache->Hkv), cache->d));
   if (ok != DT_OK) return ok;
+  const size_t one = (size_t)rows * cache->d * (dt == DT_F32 ? 4 : 2);  // bytes of a head of all rows
+  const size_t all = one * Hq, own = one * cache->Hkv;
+  if (meets(d_out, all, d_q, 1, all, all) || meets(d_out, all, d_k_tree, 1, own, own) ||
+      meets(d_out, all, d_v_tree, 1, own, own))
+    return DT_EINVAL;
   PagedArgs a = {};
   a.q = d_q;
   a.ld_q = (int64_t)Hq * cache->d;

@@ -514,7 +514,8 @@ dt_status dt_kv_read(const dt_kv_cache* cache, const int32_t* d_page_table, int 
  *   out[row][h] = sum_j softmax_j(scale * q[row][h] . k_j) v_j,
  * head h using KV head h / (Hq / Hkv); a row that sees nothing (p < 0) is 0.
  *   d_q    [total_rows][Hq][d], rows ld_q elements apart; d_out the same,
- *          contiguous; both bf16 (dt = DT_BF16; any cache but DT_F32) or fp32
+ *          contiguous; both bf16 (dt = DT_BF16; any cache but DT_F32) or fp32;
+ *          d_out overlaps nothing that the call reads (rows of d_q: DT_EINVAL)
  *   max_rows  no request has more rows; it decides how the work is split
  *   window >= 0 (0: no window), n_sink >= 0 (ignored without a window)
  * Rows outside every request's range are left as they were.  Scores, softmax
@@ -543,6 +544,8 @@ dt_status dt_paged_attn(const void* d_q, int64_t ld_q, const int32_t* d_row_star
  * may be NULL without one.
  *   d_q, d_out [batch][Nmax+1][Hq][d]; d_k_tree, d_v_tree [batch][Nmax+1][Hkv][d]
  *   d_anc, d_depths [batch][Nmax], d_n_nodes [batch] of the dt_tree
+ *   d_out overlaps nothing that the call reads (d_q, d_k_tree, d_v_tree:
+ *   DT_EINVAL)
  * Rows > d_n_nodes[b] are left as they were.  Types, sums and errors as in
  * dt_paged_attn; a node count outside [0, Nmax] records DT_EDEVICE and is
  * clamped. */

@@ -60,3 +60,42 @@ def test_a_cache_whose_storage_has_moved_is_refused(dtype, part, grow):
                                                    ws)):
         with pytest.raises(ValueError, match="moved"):
             call()
+
+
+def at(x):
+    return ctypes.c_void_p(0x100000 + x)
+
+
+def _answers(call, code, **kw):
+    """EINVAL where code says so; else the arguments are fine, and without a device the launch fails.
+    With one it would run on addresses that are none: such a call is not made."""
+    if code:
+        assert call(**kw) == code
+    elif not torch.cuda.is_available():
+        assert call(**kw) == L.DT_ECUDA
+
+
+# 10 rows of 4 heads of 64 bf16: 512 bytes a row
+@pytest.mark.parametrize("out,ld,code", [
+    (0, 256, EINVAL), (16, 256, EINVAL), (-16, 256, EINVAL), (5119 // 16 * 16, 256, EINVAL),
+    (-5120 + 16, 256, EINVAL), (5120, 256, None), (-5120, 256, None),
+    # rows of a fused projection, 8192 bytes apart: the output may lie between two of them
+    (512, 4096, None), (8192 - 5120, 4096, None), (8192 - 5120 + 16, 4096, EINVAL), (496, 4096, EINVAL),
+    (9 * 8192 + 512, 4096, None), (9 * 8192 + 496, 4096, EINVAL)])
+def test_an_output_over_the_queries_is_refused(out, ld, code):
+    """Rows that are done again read their query after outputs were written."""
+    _answers(_attn, code, q=at(0), out=at(out), ld=ld)
+
+
+# 18 rows: q 4 heads of 64 bf16 (9216 bytes), tree rows 2 heads (4608 bytes)
+@pytest.mark.parametrize("name,size", [("q", 9216), ("k", 4608), ("v", 4608)])
+def test_an_output_over_what_a_tree_call_reads_is_refused(name, size):
+    far = dict(q=at(1 << 20), k=at(2 << 20), v=at(3 << 20))
+    for x, code in ((0, EINVAL), (size - 16, EINVAL), (16 - 9216, EINVAL), (size, None), (-9216, None)):
+        _answers(_tree, code, **{**far, name: at(0)}, out=at(x))
+
+
+@pytest.mark.parametrize("dtype,out", [(L.DT_F32, 10 * 1024 - 16), (L.DT_BF16, 10 * 512 - 16)])
+def test_the_overlap_goes_by_the_type(dtype, out):
+    _answers(_attn, EINVAL, q=at(0), out=at(out), ld=256, dt=dtype)
+    _answers(_attn, None, q=at(0), out=at(out + 16), ld=256, dt=dtype)
