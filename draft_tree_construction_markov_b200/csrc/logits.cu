@@ -120,7 +120,11 @@ __global__ void __launch_bounds__(kLgThreads, 5) logits_kernel(LogitsArgs a) {
   __syncthreads();
   if (a.hist) {
     const int2 r = list_range(a.hist_start, b, a.n_hist, a.status);
-    const int np = a.n_prompt ? min(max(a.n_prompt[b], 0), r.y - r.x) : 0;
+    int np = a.n_prompt ? a.n_prompt[b] : 0;
+    if (np < 0 || np > r.y - r.x) {
+      set_status(a.status, DT_EDEVICE);
+      np = min(max(np, 0), r.y - r.x);
+    }
     for (int i0 = r.x + tid; i0 < r.y; i0 += 4 * kLgThreads) {
       int x4[4];  // (four loads on their way)
 #pragma unroll

@@ -590,7 +590,8 @@ dt_status dt_tree_verify_attn_paged(const void* d_q, const dt_kv_cache* cache,
  *            b * (Nmax+1) + i with d_mask_row NULL
  * Rows > d_n_nodes[b] of d_out are left as they were.  Tokens outside [0, V),
  * ranges outside their arrays, and mask rows outside [-1, n_mask_rows) record
- * DT_EDEVICE and are ignored.  Limits: Nmax <= 64, batch <= 1024, V < 2^24. */
+ * DT_EDEVICE and are ignored; prompt lengths outside [0, the history's] and
+ * node counts outside [0, Nmax] record it and are clamped.  Limits: Nmax <= 64, batch <= 1024, V < 2^24. */
 size_t dt_logits_workspace_bytes(void);
 
 dt_status dt_logits_process(const void* d_logits, dt_dtype dt, const int32_t* d_tokens,
