@@ -492,6 +492,14 @@ def logits_workspace_bytes() -> int:
     return int(_lib.lib.dt_logits_workspace_bytes())
 
 
+def _list(where, name, t, by, dev, dtype, *shape):
+    """Address of an optional list that ``by`` points into.  An empty one has none: ``by``'s own
+    stands for it, and is not read as a list of no entries."""
+    if t is not None and t.numel() == 0:
+        return by.data_ptr()
+    return _opt(where, name, t, dev, dtype, *shape)
+
+
 def logits_process(logits, out, ws, *, tokens=None, anc=None, n_nodes=None, history=None,
                    history_start=None, n_prompt=None, repetition=None, presence=None,
                    frequency=None, bias_start=None, bias_token=None, bias_value=None, mask=None,
@@ -501,13 +509,14 @@ def logits_process(logits, out, ws, *, tokens=None, anc=None, n_nodes=None, hist
     mask [rows, ceil(V / 32)] int32 words, one bit per allowed token."""
     where, dev = "logits_process", logits.get_device()
     batch, n1, V = logits.shape
-    # empty lists are no lists
-    if history is not None and history.numel() == 0:
-        history = history_start = n_prompt = None
-    if bias_token is not None and bias_token.numel() == 0:
-        bias_start = bias_token = bias_value = None
-    if mask is not None and mask.numel() == 0:
-        mask = mask_row = None
+    # an empty list that nothing points into is no list
+    empty = lambda t, by: t is not None and by is None and t.numel() == 0
+    if empty(history, history_start):
+        history = n_prompt = None
+    if empty(bias_token, bias_start):
+        bias_token = bias_value = None
+    if empty(mask, mask_row):
+        mask = None
     n = lambda t: 0 if t is None else t.shape[0]
     n_hist, n_bias, n_mask = n(history), n(bias_token), n(mask)
     _run(_lib.lib.dt_logits_process, where, dev, stream,
@@ -516,16 +525,16 @@ def logits_process(logits, out, ws, *, tokens=None, anc=None, n_nodes=None, hist
          _opt(where, "tokens", tokens, dev, _I32, batch, n1 - 1),
          _opt(where, "anc", anc, dev, _I64, batch, n1 - 1),
          _opt(where, "n_nodes", n_nodes, dev, _I32, batch), batch, n1 - 1, V,
-         _opt(where, "history", history, dev, _I32, n_hist),
+         _list(where, "history", history, history_start, dev, _I32, n_hist),
          _opt(where, "history_start", history_start, dev, _I32, batch + 1),
          _opt(where, "n_prompt", n_prompt, dev, _I32, batch), n_hist,
          _opt(where, "repetition", repetition, dev, _F32, batch),
          _opt(where, "presence", presence, dev, _F32, batch),
          _opt(where, "frequency", frequency, dev, _F32, batch),
          _opt(where, "bias_start", bias_start, dev, _I32, batch + 1),
-         _opt(where, "bias_token", bias_token, dev, _I32, n_bias),
-         _opt(where, "bias_value", bias_value, dev, _F32, n_bias), n_bias,
-         _opt(where, "mask", mask, dev, _I32, n_mask, (V + 31) // 32),
+         _list(where, "bias_token", bias_token, bias_start, dev, _I32, n_bias),
+         _list(where, "bias_value", bias_value, bias_start, dev, _F32, n_bias), n_bias,
+         _list(where, "mask", mask, mask_row, dev, _I32, n_mask, (V + 31) // 32),
          _opt(where, "mask_row", mask_row, dev, _I32, batch, n1), n_mask,
          _arg(where, "out", out, dev, logits.dtype, batch, n1, V), *_workspace(where, ws, dev))
     return out

@@ -35,3 +35,26 @@ def test_a_prompt_length_outside_its_history_is_recorded_and_clamped(n_prompt, a
     for i, t in enumerate((7, 8, 5)):
         want[1, 0, t] = 0.5 if i < as_if else 0.25
     assert torch.equal(out, want)
+
+
+def _empty(dtype=torch.int32, *more):
+    return torch.empty(0, *more, dtype=dtype, device="cuda")
+
+
+@pytest.mark.parametrize("args,status", [
+    (dict(history=lambda: _empty(), history_start=lambda: _i32([0, 0, 0])), 0),
+    (dict(history=lambda: _empty(), history_start=lambda: _i32([0, 0, 2])), EDEVICE),
+    (dict(history=lambda: _empty(), history_start=lambda: _i32([0, 0, 0]), n_prompt=lambda: _i32([0, 3])), EDEVICE),
+    (dict(history=lambda: _empty(), history_start=lambda: None, n_prompt=lambda: _i32([0, 3])), 0),
+    (dict(bias_token=lambda: _empty(), bias_value=lambda: _empty(torch.float32), bias_start=lambda: _i32([0, 0, 0])), 0),
+    (dict(bias_token=lambda: _empty(), bias_value=lambda: _empty(torch.float32), bias_start=lambda: _i32([0, 1, 1])),
+     EDEVICE),
+    (dict(mask=lambda: _empty(torch.int32, 2)), 0),
+    (dict(mask=lambda: _empty(torch.int32, 2), mask_row=lambda: _i32([[-1], [-1]])), 0),
+    (dict(mask=lambda: _empty(torch.int32, 2), mask_row=lambda: _i32([[-1], [0]])), EDEVICE)])
+def test_what_points_into_an_empty_list_is_read(args, status):
+    x = torch.randn(2, 1, 40, device="cuda")
+    out, ws = torch.zeros_like(x), dt.workspace(dt.logits_workspace_bytes())
+    dt.logits_process(x, out, ws, repetition=_f32(2, 2), **{k: f() for k, f in args.items()})
+    assert dt.read_status(ws) == status
+    assert torch.equal(out, x)
