@@ -1,10 +1,10 @@
-"""GPU tests of ranges that do not fit, in the lists of the logits processing.  Compared on the device
-before any use."""
+"""GPU tests of ranges: prompt lengths and lists of the logits processing that do not fit, and which
+request of many a row of the cache belongs to.  Compared on the device before any use."""
 import numpy as np
 import pytest
 import torch
 
-from tests.serving_util import cuda
+from tests.serving_util import DTYPES, cuda, page_table, to_codes
 
 pytestmark = pytest.mark.gpu
 
@@ -58,3 +58,53 @@ def test_what_points_into_an_empty_list_is_read(args, status):
     dt.logits_process(x, out, ws, repetition=_f32(2, 2), **{k: f() for k, f in args.items()})
     assert dt.read_status(ws) == status
     assert torch.equal(out, x)
+
+
+# --------------------------------------------------- rows of many requests --
+def _lens(g, batch, kind):
+    """Rows a request: some of none at the front, in runs and at the end."""
+    n = g.integers(1, 4, batch)
+    if kind == "gaps":
+        n[: batch // 5] = 0
+        n[-(batch // 7) - 1 :] = 0
+        n[batch // 3 : batch // 2] = 0
+        n[batch // 2] = 5
+    elif kind == "one":
+        n[:] = 0
+        n[g.integers(0, batch)] = 3
+    return n
+
+
+@pytest.mark.parametrize("kind", ["all", "gaps", "one"])
+@pytest.mark.parametrize("batch", [31, 32, 33, 64, 65, 333, 1024])
+def test_rows_of_many_requests_go_to_their_own_pages(batch, kind):
+    g = np.random.default_rng(batch)
+    page, hkv, d, lead = 8, 1, 64, 3
+    n = _lens(g, batch, kind)
+    pos = g.integers(0, 12, batch)
+    table, pool = page_table(g, pos + n, page)
+    start = (lead + np.concatenate([[0], np.cumsum(n)])).astype(np.int32)   # row_start[0] > 0
+    total = int(start[-1]) + 2
+    x = torch.randn(total, hkv, d, generator=torch.Generator().manual_seed(batch)).to(torch.bfloat16)
+    q, s = to_codes(x.float().numpy(), "i8")
+    cache = dt.KVCache.empty(pool, page, hkv, d, DTYPES["i8"])
+    want, want_s = torch.zeros_like(cache.k, device="cpu"), torch.zeros_like(cache.k_scale, device="cpu")
+    back = torch.full((total, hkv, d), 9.0)
+    for b in range(batch):
+        for i in range(n[b]):
+            p, r = int(pos[b]) + i, start[b] + i
+            want[table[b, p // page], :, p % page] = q[r]
+            want_s[table[b, p // page], :, p % page] = s[r]
+            back[r] = q[r].float() * s[r][..., None]
+    ws, dx = dt.workspace(dt.kv_workspace_bytes()), x.cuda()
+    where = (_i32(start), _i32(pos))
+    dt.kv_write(dx, -dx, *where, cache, cuda(table), ws)
+    assert dt.read_status(ws) == 0
+    assert torch.equal(cache.k.cpu(), want) and torch.equal(cache.v.cpu(), -want)
+    assert torch.equal(cache.k_scale.cpu(), want_s) and torch.equal(cache.v_scale.cpu(), want_s)
+    k, v = (torch.full((total, hkv, d), 9.0, device="cuda") for _ in "kv")
+    dt.kv_read(cache, cuda(table), *where, k, v, ws)
+    assert dt.read_status(ws) == 0
+    assert torch.equal(k.cpu(), back)
+    assert torch.equal(v.cpu()[lead : start[-1]], -back[lead : start[-1]])
+    assert torch.all(v[:lead] == 9) and torch.all(v[int(start[-1]) :] == 9)
