@@ -378,6 +378,12 @@ static __device__ __noinline__ void paged_row(const PagedArgs& a, int b, int i, 
     q[x] = x < per ? X::get(qp[lane * per + x]) : 0.f;
     o[x] = 0.f;
   }
+  // a stored code, as the tiled kernels of bf16 queries count it (codes_to_bf16)
+  auto code = [](typename C::T x) {
+    if constexpr (CT == DT_E4M3 && DT == DT_BF16)
+      if ((x & 0x7f) == 0x7f) return x & 0x80 ? -480.f : 480.f;
+    return C::get(x);
+  };
   float m = -INFINITY, l = 0.f;
   // this lane's key times the query (every lane takes part in the shuffles)
   auto dot = [&](auto* row, auto get) {
@@ -419,7 +425,7 @@ static __device__ __noinline__ void paged_row(const PagedArgs& a, int b, int i, 
       }
       const typename C::T* key =
           slot >= 0 ? (const typename C::T*)a.c.k + slot * a.d : nullptr;
-      float s = dot(key, C::get) * a.scale;
+      float s = dot(key, code) * a.scale;
       if (a.c.ks && slot >= 0) s *= a.c.ks[slot];
       step(ok, s, [&](int k, float p) {
         const int64_t at = __shfl_sync(0xffffffffu, slot, k);
@@ -428,7 +434,7 @@ static __device__ __noinline__ void paged_row(const PagedArgs& a, int b, int i, 
         if (a.c.vs) p *= a.c.vs[at];
 #pragma unroll
         for (int x = 0; x < 4; ++x)
-          if (x < per) o[x] = fmaf(p, C::get(v[x]), o[x]);
+          if (x < per) o[x] = fmaf(p, code(v[x]), o[x]);
       });
     }
   }

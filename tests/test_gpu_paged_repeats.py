@@ -177,3 +177,39 @@ def test_sums_that_pass_fp32_only_over_the_maximum_in_use(rows):
     assert dt.read_status(c.ws) == 0
     got = values(c.out)
     assert np.all(np.abs(got - 2.0 ** 119) <= 2.0 ** 119 * (2.0 ** -7 + 2.0 ** -14))
+
+
+@pytest.mark.parametrize("seed", [1, 2])
+def test_a_code_that_is_no_number_counts_alike_in_a_row_done_again(seed):
+    """The e4m3 codes 0x7f and 0xff count as +-480, in K and in V: also for a tree row that is done
+    again because of a row of the tree that it does not see."""
+    g = np.random.default_rng(seed)
+    L, nmax, hq, hkv, d, page = 100, 12, 4, 1, 64, 32
+    pool = Pool(g, [L], page, hkv, d, "e4m3")
+    for t, cols in ((pool.cache.k, 3), (pool.cache.v, 7)):
+        t.view(torch.uint8)[:, :, 5, cols] = 0x7F
+        t.view(torch.uint8)[:, :, 9, cols] = 0xFF
+    # small keys' scales: a score of 480 must not take the whole softmax
+    pool.cache.k_scale.mul_(0.02)
+    host = []
+    for t, s in ((pool.cache.k, pool.cache.k_scale), (pool.cache.v, pool.cache.v_scale)):
+        x = t.float().cpu()
+        x[:, :, 5] = torch.nan_to_num(x[:, :, 5], nan=480.0)
+        x[:, :, 9] = torch.nan_to_num(x[:, :, 9], nan=-480.0)
+        host.append((x.double().numpy(), values(s)))
+    k, v = (oracle.gather(x, s, pool.table[0], L) for x, s in host)
+    _, depth, anc = random_tree(g, nmax)
+    q, q64 = _q(g, (1, nmax + 1, hq, d), "bf16")
+    kt, kt64 = _q(g, (1, nmax + 1, hkv, d), "bf16")
+    vt, vt64 = _q(g, (1, nmax + 1, hkv, d), "bf16")
+    bad = 4
+    vt[0, bad + 1] = float("nan")
+    out = torch.zeros_like(q)
+    ws = dt.workspace(dt.verify_paged_workspace_bytes(1, nmax, hq, hkv, d))
+    dt.tree_verify_attn_paged(q, pool.cache, cuda(pool.table), cuda(np.array([L], np.int32)), kt, vt,
+                              cuda(anc[None].view(np.int64)), cuda(np.array([nmax], np.int32)), 0.125, out, ws)
+    o, mag, big = oracle.tree(q64[0], k, v, kt64[0], vt64[0], anc, depth, nmax, L, 0, 0, 0.125)
+    below = np.array([False] + [bool((int(a) >> bad) & 1) for a in anc])
+    tol = _bound(o, mag, big, d, L + nmax + 1, "bf16")
+    assert (~below).sum() >= 2
+    assert np.all(np.abs(values(out)[0] - o)[~below] <= tol[~below])
