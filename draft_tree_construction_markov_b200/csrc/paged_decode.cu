@@ -7,7 +7,7 @@
 // units, a ring of key pieces in shared memory that one lane of the CTA's
 // loader warp keeps filled by TMA, its own running maximum, and its own
 // accumulators; warps never wait for one another, and what shares cut is joined
-// from fp32 partials (paged_join_kernel).
+// from fp32 partials (paged_join_kernel), which also repeats rows key by key.
 //
 // The products are the warp's mma.sync, with the keys on the M axis: a
 // 128-row tcgen05 tile would be empty but for 4 or 8 rows, and its operands
@@ -505,7 +505,11 @@ __global__ void __launch_bounds__(DecShape<D, CT, NT>::kThreads, 1)
             }
           }
         }
-      for (__syncwarp(); again; again &= again - 1) {
+      // Rows to repeat are left to the join, which no ring waits for: 16 rows over 200
+      // thousand positions would take longer here than the loader waits.  Without a join no
+      // request is longer than 128 positions.
+      if (again && shift != 30 && lane == 0) a.redo[me] = 1;
+      for (__syncwarp(); again && shift == 30; again &= again - 1) {
         const int mm = c.t.m0 + __ffs(again) - 1;
         paged_row<CT, DT_BF16>(a, c.b, mm / a.G, c.kvh * a.G + mm % a.G);
       }

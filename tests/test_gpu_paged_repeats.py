@@ -213,3 +213,39 @@ def test_a_code_that_is_no_number_counts_alike_in_a_row_done_again(seed):
     tol = _bound(o, mag, big, d, L + nmax + 1, "bf16")
     assert (~below).sum() >= 2
     assert np.all(np.abs(values(out)[0] - o)[~below] <= tol[~below])
+
+
+@pytest.mark.parametrize("late", [False, True])
+def test_long_rows_done_again_hold_no_worker_up(late):
+    """420 requests of 16 (row, head) pairs share one context of 250 thousand positions, so that a
+    worker has whole row tiles.  A position that is not a number, seen by all rows or (the last one)
+    by half of them: no wait may run out meanwhile, and rows that do not see it are as they were."""
+    g = np.random.default_rng(1)
+    L, batch, rows, hkv, d, page = 250000 if not late else 60000, 420, 2, 8, 64, 256
+    pages = -(-L // page)
+    cache = dt.KVCache.empty(pages, page, hkv, d, torch.bfloat16)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    cache.k.normal_(generator=gen)
+    cache.v.normal_(generator=gen)
+    flat = lambda t: values(t.transpose(1, 2).reshape(-1, hkv, d)[:L])
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").expand(batch, -1).contiguous()
+    q, q64 = _q(g, (batch * rows, 64, d), "bf16")
+    out = torch.zeros_like(q)
+    at = L - 1 if late else 5
+    k, v = flat(cache.k), flat(cache.v)
+    cache.v[at // page, :, at % page, 3] = float("nan")
+    ws = dt.workspace(dt.paged_attn_workspace_bytes(batch, batch * rows, 64, hkv, d))
+    dt.paged_attn(q, cuda(np.arange(batch + 1, dtype=np.int32) * rows), cache, table,
+                  cuda(np.full(batch, L, np.int32)), 0.125, out, ws, max_rows=rows)
+    assert dt.read_status(ws) == 0
+    got = torch.isnan(out).view(batch, rows, 64, d)
+    assert got[:, 1, :, 3].all() and got[:, 0, :, 3].all() != late
+    got[..., 3] = False
+    assert not got.any()
+    b = 200
+    see = np.stack([oracle.seen_positions(L - rows + i, L, 0, 0) for i in range(rows)])
+    o, mag, big = oracle.attend(q64[b * rows : (b + 1) * rows, :8], k[:, :1], v[:, :1], see, 0.125)
+    err = np.abs(values(out)[b * rows : (b + 1) * rows, :8] - o) - _bound(o, mag, big, d, L, "bf16")
+    assert np.all(np.delete(err, 3, -1) <= 0)
+    if late:
+        assert np.all(err[0] <= 0)
