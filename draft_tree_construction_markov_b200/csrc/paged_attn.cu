@@ -30,7 +30,12 @@ __global__ void __launch_bounds__(32 * kPlainWarps) paged_plain_kernel(PagedArgs
 }
 
 // Rows that worker `me` finished and that came out infinite or NaN: again, key by
-// key (see paged_row).
+// key (see paged_row), where that can give anything else.  It can where a value that
+// the row does not see may be the cause (hides_odd), and where an output is infinite:
+// weights may be 2^8 over the maximum in use, and a sum may have passed fp32 for that
+// alone.  (A NaN scale that all rows see would otherwise cost every later call of its
+// request a repeat of all rows: 4.6 ms instead of 0.05 ms for a token over 8000
+// positions.)
 template <int CT>
 __device__ __noinline__ void join_redo(const PagedArgs& a, Cut cut, int me, int most) {
   __shared__ int64_t sums[kMaxKvBatch + 1];
@@ -46,9 +51,15 @@ __device__ __noinline__ void join_redo(const PagedArgs& a, Cut cut, int me, int 
       for (int r = threadIdx.x >> 5; r < c.t.live; r += kJoinWarps) {
         const int i = (c.t.m0 + r) / a.G, h = c.kvh * a.G + (c.t.m0 + r) % a.G;
         const uint16_t* out = (const uint16_t*)a.out + (((int64_t)c.rq.r0 + i) * a.Hq + h) * a.d;
-        bool odd = false;
-        for (int e = lane; e < a.d; e += 32) odd |= (out[e] & 0x7f80u) == 0x7f80u;
-        if (__any_sync(0xffffffffu, odd)) paged_row<CT, DT_BF16>(a, c.b, i, h);
+        bool odd = false, infinite = false;
+        for (int e = lane; e < a.d; e += 32) {
+          odd |= (out[e] & 0x7f80u) == 0x7f80u;
+          infinite |= (out[e] & 0x7fffu) == 0x7f80u;
+        }
+        if (!__any_sync(0xffffffffu, odd)) continue;
+        if (__any_sync(0xffffffffu, infinite) ||
+            hides_odd<CT>(a, c.rq, c.t, c.b, c.kvh, c.t.m0 + r))
+          paged_row<CT, DT_BF16>(a, c.b, i, h);
       }
     }
     left -= c.t.units - c.u;
@@ -180,8 +191,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
           sees ? make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv))
                : make_uint2(0u, 0u);
     const float odd = o.x * 0.f + o.y * 0.f + o.z * 0.f + o.w * 0.f;
-    if (__any_sync(0xffffffffu, sees && odd != 0.f && l - l == 0.f))
-      paged_row<CT, DT_BF16>(a, sp.b, i, h);
+    if (__any_sync(0xffffffffu, sees && odd != 0.f && l - l == 0.f)) {  // (as in join_redo)
+      const PagedRequest rq = paged_request(a, sp.b);
+      const float most = fmaxf(fmaxf(fabsf(o.x), fabsf(o.y)), fmaxf(fabsf(o.z), fabsf(o.w)));
+      if (__any_sync(0xffffffffu, most == INFINITY) ||
+          hides_odd<CT>(a, rq, row_tile(a, rq, sp.m0 / cut.per, cut), sp.b, sp.kvh, sp.m0 + r))
+        paged_row<CT, DT_BF16>(a, sp.b, i, h);
+    }
   }
 }
 

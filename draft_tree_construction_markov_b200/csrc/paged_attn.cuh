@@ -467,6 +467,55 @@ static __device__ __noinline__ void paged_row(const PagedArgs& a, int b, int i, 
   }
 }
 
+// Can a value that pair m of row tile t (its (token, head) pair) does not see have made its sums
+// infinite or NaN?  The products of a tile include what lies beside the tile's
+// visible positions in the same 128 (no kernel here has larger tiles), up to the request's last
+// one, and all rows of its tree: this looks whether such a value (of a quantised cache: its
+// scale, for the codes are finite) is infinite or NaN.  Where none is, the row's sums are what it
+// sees, and a repeat would only give them again.  Whole warps.
+template <int CT>
+static __device__ __noinline__ bool hides_odd(const PagedArgs& a, const PagedRequest& rq,
+                                              const RowTile& t, int b, int kvh, int m) {
+  const int lane = threadIdx.x & 31, i = m / a.G;
+  const Visible vis = visible(a, row_position(a, rq, b, i), rq.len);
+  // d values of a row in bf16, by the whole warp
+  auto odd_row = [&](const uint16_t* row) {
+    bool odd = false;
+    for (int e = lane; e < a.d / 2; e += 32) {
+      const uint32_t w = ((const uint32_t*)row)[e];
+      odd |= (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+    }
+    return odd;
+  };
+  bool odd = false;
+  auto positions = [&](int lo, int hi) {
+    if constexpr (CT == DT_BF16) {
+#pragma unroll 8
+      for (int j = lo; j < hi; ++j) {
+        const int64_t s = a.c.slot(b, j, nullptr);  // (a page that no row needs may be none)
+        if (s >= 0)
+          odd |= odd_row((const uint16_t*)a.c.v + (s + ((int64_t)kvh << a.c.page_shift)) * a.d);
+      }
+    } else {
+      for (int j = lo + lane; j < hi; j += 32) {
+        const int64_t s = a.c.slot(b, j, nullptr);
+        if (s >= 0) odd |= !(fabsf(a.c.vs[s + ((int64_t)kvh << a.c.page_shift)]) < INFINITY);
+      }
+    }
+  };
+  const int lo = t.lo & ~127, hi = min((t.hi + 127) & ~127, rq.len);
+  positions(vis.sink, min(min((t.sink + 127) & ~127, rq.len), vis.first));
+  positions(max(lo, vis.sink), vis.first);
+  positions(max(lo, vis.last), hi);
+  if (a.kt) {
+    const uint64_t anc = i ? a.anc[(int64_t)b * a.Nmax + i - 1] : 0ull;
+    for (int j = 0; j < rq.n; ++j)
+      if (!tree_sees(anc, i, j))
+        odd |= odd_row((const uint16_t*)a.vt + (((int64_t)rq.r0 + j) * a.c.Hkv + kvh) * a.d);
+  }
+  return __any_sync(0xffffffffu, odd);
+}
+
 // Tensor map of rows of `cols` elements of `bytes` (2: bf16, 1: codes), boxes of
 // min(cols * bytes, 128) bytes x `box` rows, swizzled over their width.
 bool paged_map(CUtensorMap* m, const void* base, int bytes, uint64_t cols, uint64_t rows,

@@ -121,6 +121,35 @@ def test_such_scales_beside_a_tree(code, nmax):
         assert np.all(err <= _bound(o, mag, big, d, L + nmax + 1, "bf16"))
 
 
+@pytest.mark.parametrize("code", ["bf16", "e4m3", "i8"])
+@pytest.mark.parametrize("rows,at", [(1, 900), (4, 900), (4, 7990), (40, 100), (200, 2900)])
+def test_what_every_row_sees_is_not_done_again(code, rows, at):
+    """A position that is not a number and that all rows of the request see: NaN it is, at once.
+    (A bf16 cache: in one column, and the others are as they would be without it.)"""
+    lens = [8000, 3000] if rows < 40 else [4000, 3000]
+    c = Chunk(np.random.default_rng(at), lens, rows, code)
+    k, v = c.pool.rows(0, lens[0])
+    clean = c.ms()
+    p, s = int(c.pool.table[0, at // c.page]), at % c.page
+    if code == "bf16":
+        c.pool.cache.v[p, :, s, 5] = float("nan")
+    else:
+        c.pool.cache.v_scale[p, :, s] = float("nan")
+    assert c.ms() <= 3 * clean + 0.5
+    got = values(c.out)
+    nan = np.isnan(got[:rows])
+    assert np.isfinite(got[rows:]).all()
+    if code != "bf16":
+        assert nan.all()
+        return
+    assert nan[..., 5].all() and not np.delete(nan, 5, -1).any()
+    pick = np.unique([0, rows // 2, rows - 1])
+    see = np.stack([oracle.seen_positions(lens[0] - rows + i, lens[0], 0, 0) for i in pick])
+    o, mag, big = oracle.attend(c.q64[pick], k, v, see, c.d ** -0.5)
+    err = np.delete(np.abs(got[pick] - o) - _bound(o, mag, big, c.d, lens[0], "bf16"), 5, -1)
+    assert np.all(err <= 0)
+
+
 @pytest.mark.parametrize("window,sink,at", [(1000, 0, 4000 - 4 - 1000), (1000, 70, 69), (1000, 70, 70),
                                             (333, 5, 4000 - 2 - 333)])
 @pytest.mark.parametrize("rows,hq,hkv", [(4, 8, 2), (1, 8, 2), (60, 8, 1)])
