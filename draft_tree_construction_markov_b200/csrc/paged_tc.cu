@@ -243,8 +243,8 @@ struct TcShape {
   static constexpr int kPerSm = NQ == 2 ? 1 : 2;
   // TMEM columns: S at 128 q, O at 128 NQ + D q, P where neither is.  Only for D = 128 with
   // tiles of 128 keys is there no room left: P then lies over the upper half of S.  The next S
-  // follows the product that reads P in the pipe, with the same shape, and reaches these columns
-  // last.
+  // follows the product that reads P in the pipe, and products of one shape (here 128 x 128
+  // both) are carried out in the order of their issue.  Of other shapes that is not promised.
   static constexpr uint32_t kTmemCols = NQ == 2 ? 512 : 256;
   static constexpr uint32_t p_at(uint32_t q) {
     return D == 128 && KT == 128 ? 128 * q + 64 : NQ == 2 ? 384 + 64 * q : KT == 64 ? 64 : 192;
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
           wait_all(&i_full[ni % S::kItems], (ni / S::kItems) & 1);
           pairs = items[ni % S::kItems].live > 128 ? 2 : 1;
           in_item = items[ni % S::kItems].seg;
-          __syncwarp();
+          __syncwarp();  // (the schedule writes items by plain stores, which an arrive does order)
           if (one) free_item(ni);
           ++ni;
         };
@@ -601,8 +601,12 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
             fence_async_smem();
             mbar_arrive(part ? v_full : k_full);
             if (part == 0) mbar_arrive(&c_full[g % S::kScales]);
-            // The codes' place is free only now: told so before the wait for the operand's
-            // place, the next copy could arrive before the loads above had been carried out.
+            // The codes' place is freed once the codes have been used and behind the fence: an
+            // arrive alone orders this thread's loads before other threads' loads and stores,
+            // not before a copy's writes (the async proxy).  An earlier form arrived between the
+            // loads and the wait for the operand's place and, with P over scores of another
+            // shape (p_at), gave wrong outputs under load.  Both were changed in one step; which
+            // of the two was seen there has not been established, and neither is promised to work.
             __syncwarp();
             if (lane == 0) mbar_arrive(&w_empty[st]);
           }
