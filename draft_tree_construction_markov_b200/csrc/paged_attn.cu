@@ -76,6 +76,7 @@ template <int CT>
 __global__ void __launch_bounds__(32 * kJoinWarps)
     paged_join_kernel(const __grid_constant__ PagedArgs a, Cut cut, int workers) {
   __shared__ float4 sums[kJoinWarps][32];
+  static_assert(kDecodeWorkers >= 2 * kPagedSms);
   __shared__ int before[kDecodeWorkers + 1];  // tasks before worker w
   __shared__ int carry[kJoinWarps];
   pdl_wait();
@@ -233,8 +234,12 @@ PartPlan part_plan(int64_t workers, int64_t rows, int d) {
   p.bytes = kWsHeader + p.stats + 2 * workers * rows * sizeof(float2);
   return p;
 }
-size_t paged_workspace(int64_t all, int d) {
-  return std::max(part_plan(2 * kPagedSms, std::min<int64_t>(all, 128), d).bytes,
+// (two row tiles a CTA take half the workers, so no more); trees never take the kernel of few rows
+size_t tree_workspace(int64_t all, int d) {
+  return part_plan(2 * kPagedSms, std::min<int64_t>(all, 128), d).bytes;
+}
+size_t chunk_workspace(int64_t all, int d) {
+  return std::max(tree_workspace(all, d),
                   part_plan(kDecodeWorkers, std::min<int64_t>(all, kDecodePairs), d).bytes);
 }
 
@@ -336,7 +341,7 @@ extern "C" {
 
 size_t dt_paged_attn_workspace_bytes(int batch, int total_rows, int Hq, int Hkv, int d) {
   if (batch < 1 || total_rows < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || d < 1) return 0;
-  return paged_workspace((int64_t)total_rows * (Hq / Hkv), d);
+  return chunk_workspace((int64_t)total_rows * (Hq / Hkv), d);
 }
 
 dt_status dt_paged_attn(const void* d_q, int64_t ld_q, const int32_t* d_row_start,
@@ -351,7 +356,7 @@ dt_status dt_paged_attn(const void* d_q, int64_t ld_q, const int32_t* d_row_star
   if (!d_row_start || !d_kv_len || total_rows < 0 || max_rows < 1) return DT_EINVAL;
   if (ld_q < (int64_t)Hq * cache->d || (ld_q * (dt == DT_F32 ? 4 : 2)) % 16) return DT_EINVAL;
   if ((int64_t)total_rows * Hq >= (int64_t)1 << 30) return DT_EUNSUPPORTED;
-  ok = check_ws(ws, ws_bytes, paged_workspace((int64_t)total_rows * (Hq / cache->Hkv), cache->d));
+  ok = check_ws(ws, ws_bytes, chunk_workspace((int64_t)total_rows * (Hq / cache->Hkv), cache->d));
   if (ok != DT_OK) return ok;
   const size_t es = dt == DT_F32 ? 4 : 2, row = (size_t)Hq * cache->d * es;
   if (meets(d_out, total_rows * row, d_q, total_rows, ld_q * es, row)) return DT_EINVAL;
@@ -377,7 +382,7 @@ dt_status dt_paged_attn(const void* d_q, int64_t ld_q, const int32_t* d_row_star
 
 size_t dt_tree_verify_attn_paged_workspace_bytes(int batch, int Nmax, int Hq, int Hkv, int d) {
   if (batch < 1 || Nmax < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || d < 1) return 0;
-  return paged_workspace((int64_t)(Nmax + 1) * (Hq / Hkv), d);
+  return tree_workspace((int64_t)(Nmax + 1) * (Hq / Hkv), d);
 }
 
 dt_status dt_tree_verify_attn_paged(const void* d_q, const dt_kv_cache* cache,
@@ -399,7 +404,7 @@ dt_status dt_tree_verify_attn_paged(const void* d_q, const dt_kv_cache* cache,
   if (Nmax > 64 || (window && window <= Nmax)) return DT_EUNSUPPORTED;
   const int rows = batch * (Nmax + 1);
   if ((int64_t)rows * Hq >= (int64_t)1 << 30) return DT_EUNSUPPORTED;
-  ok = check_ws(ws, ws_bytes, paged_workspace((int64_t)(Nmax + 1) * (Hq / cache->Hkv), cache->d));
+  ok = check_ws(ws, ws_bytes, tree_workspace((int64_t)(Nmax + 1) * (Hq / cache->Hkv), cache->d));
   if (ok != DT_OK) return ok;
   const size_t one = (size_t)rows * cache->d * (dt == DT_F32 ? 4 : 2);  // bytes of a head of all rows
   const size_t all = one * Hq, own = one * cache->Hkv;

@@ -530,6 +530,7 @@ cudaError_t launch_paged_tc(const PagedArgs& a, int ct, const dt_kv_cache* cache
 cudaError_t launch_paged_decode(const PagedArgs& a, int ct, const dt_kv_cache* cache, int pairs,
                                 cudaStream_t s);
 cudaError_t launch_paged_join(const PagedArgs& a, int ct, Cut cut, int workers, cudaStream_t s);
-constexpr int kDecodeWorkers = 15 * kPagedSms, kDecodePairs = 16;  // (the most of any type)
+constexpr int kDecodeWarps = 11;  // workers of a CTA of the kernel of few rows
+constexpr int kDecodeWorkers = kDecodeWarps * kPagedSms, kDecodePairs = 16;
 
 }  // namespace dt

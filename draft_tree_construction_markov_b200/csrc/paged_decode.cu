@@ -40,8 +40,7 @@ template <int D, int CT, int NT>
 struct DecShape {
   static constexpr int kBytes = CT == DT_BF16 ? 2 : 1;
   static constexpr int kKeys = CT == DT_BF16 ? 16 : 32;  // positions of a piece
-  // workers of a CTA: codes take instructions, and more warps hide their latency; bf16 takes bytes
-  static constexpr int kWarps = 11;
+  static constexpr int kWarps = kDecodeWarps;
   static constexpr int kRow = D * kBytes;                // bytes of a key
   static constexpr int KC = kRow > 128 ? kRow / 128 : 1; // 128-byte columns of the ring
   static constexpr int kWidth = kRow / KC;               // bytes of a row in one of them

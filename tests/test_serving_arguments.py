@@ -99,3 +99,16 @@ def test_an_output_over_what_a_tree_call_reads_is_refused(name, size):
 def test_the_overlap_goes_by_the_type(dtype, out):
     _answers(_attn, EINVAL, q=at(0), out=at(out), ld=256, dt=dtype)
     _answers(_attn, None, q=at(0), out=at(out + 16), ld=256, dt=dtype)
+
+
+def test_a_workspace_holds_what_its_call_can_leave_and_no_more():
+    """Two partials of (sums, maximum and sum of weights) a pair, for every worker: 296 blocks of row
+    tiles, or 148 blocks of 11 workers of at most 16 pairs, which trees never have; and 32 bytes of
+    records a worker, with the header and paddings below a kilobyte."""
+    part = lambda workers, pairs, d: workers * (2 * pairs * (4 * d + 8) + 32)
+    for d in (64, 128):
+        for rows, pairs in ((4, 16), (1, 4), (33, 132), (65, 260)):
+            tiles, few = part(296, min(pairs, 128), d), part(148 * 11, min(pairs, 16), d)
+            assert 0 <= dt.paged_attn_workspace_bytes(1, rows, 32, 8, d) - max(tiles, few) < 1024
+            if rows > 1:
+                assert 0 <= dt.verify_paged_workspace_bytes(1, rows - 1, 32, 8, d) - tiles < 1024
