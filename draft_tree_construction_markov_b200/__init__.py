@@ -375,10 +375,12 @@ def _table(where, cache, t):
     if (k.data_ptr() != at_k or v.data_ptr() != at_v
             or ks is not None and (ks.data_ptr() != at_ks or vs.data_ptr() != at_vs)):
         raise ValueError(f"{where}: the cache's tensors have moved; make a new KVCache")
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{where}: page_table must be [batch, max_pages]")
-    batch, pages = t.shape
-    return _arg(where, "page_table", t, cache.device, _I32, batch, pages), batch, pages
+    if t.dtype is not _I32 or t.get_device() != cache.device or not t.is_contiguous():
+        _arg(where, "page_table", t, cache.device, _I32, *shape)  # says what is wrong
+    return t.data_ptr(), *shape
 
 
 def kv_workspace_bytes() -> int:
