@@ -494,14 +494,6 @@ def logits_workspace_bytes() -> int:
     return int(_lib.lib.dt_logits_workspace_bytes())
 
 
-def _list(where, name, t, by, dev, dtype, *shape):
-    """Address of an optional list that ``by`` points into.  An empty one has none: ``by``'s own
-    stands for it, and is not read as a list of no entries."""
-    if t is not None and t.numel() == 0:
-        return by.data_ptr()
-    return _opt(where, name, t, dev, dtype, *shape)
-
-
 def logits_process(logits, out, ws, *, tokens=None, anc=None, n_nodes=None, history=None,
                    history_start=None, n_prompt=None, repetition=None, presence=None,
                    frequency=None, bias_start=None, bias_token=None, bias_value=None, mask=None,
@@ -511,33 +503,36 @@ def logits_process(logits, out, ws, *, tokens=None, anc=None, n_nodes=None, hist
     mask [rows, ceil(V / 32)] int32 words, one bit per allowed token."""
     where, dev = "logits_process", logits.get_device()
     batch, n1, V = logits.shape
-    # an empty list that nothing points into is no list
-    empty = lambda t, by: t is not None and by is None and t.numel() == 0
-    if empty(history, history_start):
-        history = n_prompt = None
-    if empty(bias_token, bias_start):
-        bias_token = bias_value = None
-    if empty(mask, mask_row):
-        mask = None
-    n = lambda t: 0 if t is None else t.shape[0]
-    n_hist, n_bias, n_mask = n(history), n(bias_token), n(mask)
+    # An empty list has no address: what points into it stands for it (the library reads no entry of
+    # it, but what points), and without that it is no list.
+    n_hist = 0 if history is None else history.shape[0]
+    n_bias = 0 if bias_token is None else bias_token.shape[0]
+    n_mask = 0 if mask is None else mask.shape[0]
+    hist_at = _opt(where, "history_start", history_start, dev, _I32, batch + 1)
+    hist = (_arg(where, "history", history, dev, _I32, n_hist) if n_hist else
+            None if history is None else hist_at)
+    if hist is None and history is not None:
+        n_prompt = None
+    bias_at = _opt(where, "bias_start", bias_start, dev, _I32, batch + 1)
+    token = (_arg(where, "bias_token", bias_token, dev, _I32, n_bias) if n_bias else
+             None if bias_token is None else bias_at)
+    value = (bias_at if bias_token is not None and not n_bias and (bias_value is None or not len(bias_value)) else
+             _opt(where, "bias_value", bias_value, dev, _F32, n_bias))
+    mask_at = _opt(where, "mask_row", mask_row, dev, _I32, batch, n1)
+    words = (_arg(where, "mask", mask, dev, _I32, n_mask, (V + 31) // 32) if n_mask else
+             None if mask is None else mask_at)
     _run(_lib.lib.dt_logits_process, where, dev, stream,
          _arg(where, "logits", logits, dev, logits.dtype, batch, n1, V),
          _float_code(where, "logits", logits),
          _opt(where, "tokens", tokens, dev, _I32, batch, n1 - 1),
          _opt(where, "anc", anc, dev, _I64, batch, n1 - 1),
          _opt(where, "n_nodes", n_nodes, dev, _I32, batch), batch, n1 - 1, V,
-         _list(where, "history", history, history_start, dev, _I32, n_hist),
-         _opt(where, "history_start", history_start, dev, _I32, batch + 1),
+         hist, hist_at,
          _opt(where, "n_prompt", n_prompt, dev, _I32, batch), n_hist,
          _opt(where, "repetition", repetition, dev, _F32, batch),
          _opt(where, "presence", presence, dev, _F32, batch),
          _opt(where, "frequency", frequency, dev, _F32, batch),
-         _opt(where, "bias_start", bias_start, dev, _I32, batch + 1),
-         _list(where, "bias_token", bias_token, bias_start, dev, _I32, n_bias),
-         _list(where, "bias_value", bias_value, bias_start, dev, _F32, n_bias), n_bias,
-         _list(where, "mask", mask, mask_row, dev, _I32, n_mask, (V + 31) // 32),
-         _opt(where, "mask_row", mask_row, dev, _I32, batch, n1), n_mask,
+         bias_at, token, value, n_bias, words, mask_at, n_mask,
          _arg(where, "out", out, dev, logits.dtype, batch, n1, V), *_workspace(where, ws, dev))
     return out
 

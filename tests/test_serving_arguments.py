@@ -112,3 +112,13 @@ def test_a_workspace_holds_what_its_call_can_leave_and_no_more():
             assert 0 <= dt.paged_attn_workspace_bytes(1, rows, 32, 8, d) - max(tiles, few) < 1024
             if rows > 1:
                 assert 0 <= dt.verify_paged_workspace_bytes(1, rows - 1, 32, 8, d) - tiles < 1024
+
+
+def test_lists_of_logits_that_do_not_belong_together_are_refused():
+    z, ws = torch.zeros(2, 1, 50), torch.zeros(256, dtype=torch.uint8)
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    for bad in (dict(bias_value=torch.zeros(3)), dict(bias_token=i(2), bias_value=torch.zeros(3), bias_start=i(3)),
+                dict(bias_token=i(0), bias_value=torch.zeros(3), bias_start=i(3)),
+                dict(history=i(0), history_start=i(2)), dict(mask=i(0, 2), mask_row=i(2))):
+        with pytest.raises(ValueError):
+            dt.logits_process(z, torch.zeros_like(z), ws, **bad)
