@@ -332,6 +332,7 @@ __global__ void __launch_bounds__(DecShape<D, CT, NT>::kThreads, 1)
           }
           // ---- mask, maximum, weights
           bool grows = false;
+          unsigned hidden = 0;  // scores that their row does not see, a bit each
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -340,7 +341,10 @@ __global__ void __launch_bounds__(DecShape<D, CT, NT>::kThreads, 1)
               if (masked) {
                 const int key = p.at + (e & 2 ? rb : ra);
                 const Visible& v = vis[nt][e & 1];
-                if (!(key < v.last && (key >= v.first || key < v.sink))) s[nt][e] = -INFINITY;
+                if (!(key < v.last && (key >= v.first || key < v.sink))) {
+                  s[nt][e] = -INFINITY;
+                  hidden |= 1u << (4 * nt + e);
+                }
               }
               grows |= s[nt][e] > m[nt][e & 1] + kDecRescale;
             }
@@ -378,7 +382,9 @@ __global__ void __launch_bounds__(DecShape<D, CT, NT>::kThreads, 1)
               w4[e] = ex2(s[nt][e] - use);
               l[nt][e & 1] += w4[e];
               if constexpr (S::kScaled)
-                w4[e] = masked && s[nt][e] == -INFINITY ? 0.f : w4[e] * (e & 2 ? vb2 : va);
+                // (what the row does not see has weight 0 whatever its scale; a score of
+                // -infinity that it does see has 0 times its scale)
+                w4[e] = (hidden >> (4 * nt + e)) & 1u ? 0.f : w4[e] * (e & 2 ? vb2 : va);
             }
             b0[nt] = transpose8x8(pack2(w4[0], w4[1]));
             b1[nt] = transpose8x8(pack2(w4[2], w4[3]));

@@ -278,3 +278,23 @@ def test_long_rows_done_again_hold_no_worker_up(late):
     assert np.all(np.delete(err, 3, -1) <= 0)
     if late:
         assert np.all(err[0] <= 0)
+
+
+@pytest.mark.parametrize("code", ["e4m3", "i8"])
+@pytest.mark.parametrize("rows,L", [(1, 33), (1, 500), (4, 500), (20, 500)])
+def test_a_seen_score_of_minus_infinity_takes_its_value_s_scale(code, rows, L):
+    """A key's scale is infinite and its value's is not a number: whatever the sign of the score (a
+    weight of 0 for some heads), the rows that see the position are NaN, and the others are not."""
+    c = Chunk(np.random.default_rng(L + rows), [L], rows, code)
+    k, v = c.pool.rows(0, L)
+    at = L - 1 if rows == 1 else L - 2
+    p, s = int(c.pool.table[0, at // c.page]), at % c.page
+    c.pool.cache.k_scale[p, :, s] = float("inf")
+    c.pool.cache.v_scale[p, :, s] = float("nan")
+    c()
+    assert dt.read_status(c.ws) == 0
+    nan = torch.isnan(c.out).flatten(1)
+    hit = torch.arange(rows, device="cuda") >= rows - (L - at)
+    assert nan[hit].all() and not nan[~hit].any()
+    if rows > 2:
+        c.check(0, k, v, np.arange(rows - 2))
