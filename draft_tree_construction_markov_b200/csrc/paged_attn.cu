@@ -2,7 +2,10 @@
 // sliding window with a few first tokens kept), or a draft tree's rows.
 //
 // This file holds the C entry points and the kernel of fp32 queries, one warp
-// per (row, head); bf16 queries take the tiled kernels.
+// per (row, head) and key by key, for checks and small sizes: it is bound by
+// latency, about 1 us a position (one token over 4096 positions, e4m3: 4.0 ms
+// against 42 us; 512 rows over 4096, bf16: 36 ms against 77 us).  bf16 queries take
+// the tiled kernels.
 #include <algorithm>
 
 #include "paged_attn.cuh"
@@ -34,7 +37,7 @@ __global__ void __launch_bounds__(32 * kPlainWarps) paged_plain_kernel(PagedArgs
 // the row does not see may be the cause (hides_odd), and where an output is infinite:
 // weights may be 2^8 over the maximum in use, and a sum may have passed fp32 for that
 // alone.  (A NaN scale that all rows see would otherwise cost every later call of its
-// request a repeat of all rows: 4.6 ms instead of 0.05 ms for a token over 8000
+// request a repeat of all rows: 5.7 ms instead of 0.07 ms for a token over 8000
 // positions.)
 template <int CT>
 __device__ __noinline__ void join_redo(const PagedArgs& a, Cut cut, int me, int most) {
@@ -268,9 +271,11 @@ dt_status run_paged(PagedArgs a, const dt_kv_cache* cache, int dt, void* ws, cud
   // cache: 110 us against 231 us with tiles).
   const bool few = !a.kt && pairs <= kDecodePairs;
   // Two row tiles share a CTA's keys where a request has more than one.  Trees up
-  // to 256 pairs keep one: their node counts vary, and most do not reach the second
-  // (64 trees of 8 to 32 nodes, 4 heads: 229 us against 273 us; one tree of 64
-  // nodes, 260 pairs: 34 us with two, 39 us with one).
+  // to 256 pairs keep one: their node counts vary, only the device knows them, and most do not
+  // reach the second.  64 trees of 8 to 32 nodes, 4 heads: 234 us over e4m3 and 155 over bf16
+  // pages with one tile, 282 and 182 with two; of 32 nodes each (132 pairs, four over a
+  // tile): 360 and 235 with one, 320 and 205 with two.  One tree of 64 nodes, 260
+  // pairs: 34 us with two, 39 us with one.
   const int tiles = pairs > (a.kt ? 256 : 128) ? 2 : 1;
   a.part_rows = (int)std::min<int64_t>(all, few ? kDecodePairs : 128 * tiles);
   const PartPlan p = part_plan(few ? kDecodeWorkers : 2 * kPagedSms / tiles, a.part_rows, a.d);

@@ -21,12 +21,17 @@
 // both products free of bank conflicts in the swizzled ring.
 // P^T is S^T's fragment transposed (movmatrix).
 //
+// The weights are rounded to bf16 for the second product, whose operands have one
+// type (see paged_tc.cu); scores, statistics, sums and partials are fp32.
+//
 // Measured (B200): 64 single tokens over 512 to 65536 positions, 32 / 8 heads of
-// 128, e4m3 cache: 372 MB in 110 us with the join, 3.4 TB/s (0.52 of the measured
-// copy rate).  What holds it up is the conversion: five integer instructions, at
-// two cycles each, for four codes (eight with neighbours paired).  Fifteen
-// workers of 16-position pieces instead of eleven of 32: 179 us, since the
-// loader's work is per piece.
+// 128, e4m3 cache: 372 MB in 111 us with the join, 3.4 TB/s (0.51 of the measured
+// copy rate); bf16 cache, 721 MB in 165 us.  With codes no unit is full: ALU 54 %
+// (the conversion, five integer instructions for four codes), issue 51 %, DRAM
+// 47 %, tensor cores 12 %.  Each of the 11 workers, fewer than three a scheduler,
+// goes through wait, load, convert, product, softmax and product one after the
+// other.  Fifteen workers of 16-position pieces instead of eleven of 32: 179 us,
+// since the loader's work is per piece.
 #include <algorithm>
 
 #include "paged_attn.cuh"

@@ -26,18 +26,27 @@
 // CTAs in equal consecutive shares; a row tile that two shares cut is joined by
 // paged_join_kernel from fp32 partials.
 //
+// P is rounded to bf16 (2^-8 of a weight at most): the operands of a product have
+// one type, which is V's, and fp16 would not hold weights times scales.  It takes
+// the outputs' error against 64 bits from 0.0017 (bf16 outputs alone) to 0.0024 of
+// their norm.  Weights in two bf16 halves would take it back for half as many
+// tensor-core cycles again.  Scores, statistics, sums and partials are fp32.
+//
 // Bound and measured (B200): three chunks of up to 2048 rows over up to 8192
-// positions, 32 / 8 heads of 128, bf16 cache: 479 GFLOP in 0.55 ms, 875 TFLOP/s
-// (0.53 of the measured peak).  2 x 128 x 128 exponentials a key tile take the
+// positions, 32 / 8 heads of 128, bf16 cache: 479 GFLOP in 0.54 ms, 885 TFLOP/s
+// (0.54 of the measured peak).  2 x 128 x 128 exponentials a key tile take the
 // SM's special-function units as long (2048 cycles) as its products the tensor
-// core; a tile takes about 3600, the rest being the two softmaxes' other
-// instructions and the wait between a softmax and the products it feeds.  The
-// same over int8 with a 4096-position window: 450 GFLOP in 0.85 ms.  There the
-// reads of the scales (96 wide shared loads a row and tile, which all lanes
-// repeat) and the conversion hold the softmax up; other forms were measured
-// and are no faster: scores in fragment layout, where a lane needs a quarter of
-// the scales but TMEM gives the same data in 74 instead of 27 cycles, 0.84 ms;
-// key tiles of 64 with all scores in registers, 1.04 ms.
+// core, and both are half busy (53 % each): a tile takes about 3600 cycles, since
+// the products wait for whole softmaxes and these for them.  The same over int8
+// with a 4096-position window: 450 GFLOP in 0.86 ms, shared-memory wavefronts 54 %
+// (the scales: 96 wide loads a row and tile, which all lanes repeat), issue 45 %,
+// ALU 39 %, tensor cores 28 %.  Other forms were measured and are no faster:
+// scores in fragment layout, where a lane needs a quarter of the scales but TMEM
+// gives the same data in 74 instead of 27 cycles, 0.84 ms; key tiles of 64 with
+// all scores in registers, 1.04 ms.  64 trees of 8 to 32 nodes over an e4m3 cache:
+// 227 us, issue 52 %, shared-memory wavefronts 49 %, ALU 41 %, tensor cores 19 %.
+// One tree of 64 nodes over 4096 positions, bf16: 33 us, of which its 260 pairs,
+// four over a row tile of two, make every key tile come twice.
 #include <algorithm>
 #include <type_traits>
 
@@ -592,9 +601,9 @@ __global__ void __launch_bounds__(TcShape<D, CT, NQ>::kThreads, TcShape<D, CT, N
             }
             // A place that no row sees may have any scale, and a weight of 0 times it need not be
             // 0: a NaN there (a pool never cleared, a page whose last owner was not finite) would
-            // send all rows of the tile to paged_row, 4.6 ms instead of 0.06 ms for a chunk over
-            // 3000 positions.  (Cleared here, before the softmax reads it; a select there, where
-            // the masks are, made the whole call 3 to 7 % longer.)
+            // send all rows of the tile to paged_row, 6.2 ms instead of 0.06 ms for three chunks of
+            // 200 rows over up to 3000 positions.  (Cleared here, before the softmax reads it; a
+            // select there, where the masks are, made the whole call 3 to 7 % longer.)
             if (part == 0 && base >= 0 && (base < lo || base + KT > hi) && (tid & 127) < KT &&
                 !it.seen(base + (tid & 127), 1))
               sscale[g % S::kScales * 2 * KT + KT + (tid & 127)] = 0.f;

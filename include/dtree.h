@@ -518,6 +518,9 @@ dt_status dt_kv_read(const dt_kv_cache* cache, const int32_t* d_page_table, int 
  *          d_out overlaps nothing that the call reads (rows of d_q: DT_EINVAL)
  *   max_rows  no request has more rows; it decides how the work is split
  *   window >= 0 (0: no window), n_sink >= 0 (ignored without a window)
+ * fp32 queries are for checks and small sizes: they take one warp per (row,
+ * head), key by key, about 1 us a position (one token over 4096 positions: 4 ms,
+ * a chunk of 512 rows over them: 36 ms; with bf16 queries 0.04 and 0.08 ms).
  * Rows outside every request's range are left as they were.  Scores, softmax
  * statistics and sums are fp32; the softmax weights (times the value's scale,
  * in a scaled cache) enter the second product as bf16 (dt = DT_BF16).  A value
