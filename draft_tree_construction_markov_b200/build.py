@@ -42,7 +42,7 @@ LAUNCH_REGS = {(1, 2): 168, (2, 1): 80, (3, 1): 80, (2, 2): 128, (3, 2): 128}
 
 def check_registers(log):
     """Raises where the compiler (its -v output) gave such a kernel another number than its shares are
-    made for: the library would refuse to launch it, and no call could run."""
+    made for: the library would refuse to launch it, and its calls would fail."""
     for d, code, tiles, regs in re.findall(
             r"Compiling entry function '\S*paged_tc_kernelILi(\d+)ELi(\d)ELi(\d)E(?:(?!Compiling entry).)*?"
             r"Used (\d+) registers", log, re.S):
